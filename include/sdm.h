@@ -60,7 +60,8 @@ typedef enum {
     SDM_ENGINE_SLOT = 2,
     SDM_ENGINE_CHUNK = 3
 } sdm_engine;
-typedef enum { SDM_INIT_FROM_M0 = 0, SDM_CONTINUE = 1 } sdm_init;
+/* SDM_INIT_ZERO is for the dense-state layer's calls (sdm_conv_forward, sdm_ssm_forward). */
+typedef enum { SDM_INIT_FROM_M0 = 0, SDM_CONTINUE = 1, SDM_INIT_ZERO = 2 } sdm_init;
 typedef enum { SDM_GATE_SILU = 0, SDM_GATE_SIGMOID = 1, SDM_GATE_IDENTITY = 2 } sdm_gate_act;
 
 /* Problem shape.  B sequences, T tokens, H heads, S1 + S2 half scores per (token, head),
@@ -321,6 +322,110 @@ sdm_status sdm_state_pack(const float *M, int64_t rows, int32_t d_v, int32_t for
 sdm_status sdm_state_unpack(const void *codes, const float *scales, int64_t rows, int32_t d_v,
                             int32_t format, float *M, void *stream);
 
+/*
+ * The dense-state layer's operators (no counterpart on the SDM pages): what a recurrent layer
+ * with a dense state runs next to the sparse memory pass in one stack of layers -- a causal
+ * short convolution over the projected channels, a selective state-space scan, and the norms
+ * around a block.  Each has a form for prompts and one for single tokens; forward only, like
+ * the pass.  The conventions at the top hold, except that
+ *  - rows may be pitched: a `*_stride` is the distance in elements between the rows of
+ *    consecutive tokens (0: contiguous; a multiple of 16 bytes except for dt), so that k, q and
+ *    v may be slices of one projected row; the rows of sequence b + 1 follow those of b;
+ *  - y has in_dtype, rounded once from fp32;
+ *  - a batch is B sequences of T tokens each, or packed: with cu (int32 [B + 1], device,
+ *    4-byte aligned) sequence b holds rows cu[b] .. cu[b + 1] - 1 of the T rows.  Sequences
+ *    may be empty; rows in no sequence are neither read nor written.  Offsets outside [0, T] are
+ *    clamped, a sequence that ends before it starts is empty, and either sets
+ *    SDM_ERR_DEVICE_CHECK in the status word.
+ * An output may overlap no input and no other output unless a call says so; overlaps are
+ * refused (SDM_ERR_INVALID_ARG), like every other bad argument, before anything is launched.
+ */
+
+/* B sequences, T tokens (rows in all when packed), C channels (a multiple of 8), K taps (2 to
+ * 4).  x_stride: see above, at least C. */
+typedef struct {
+    int32_t B, T, C, K;
+    int32_t in_dtype;
+    int64_t x_stride;
+} sdm_conv_shape;
+
+/*
+ * Causal short convolution, each channel on its own:
+ *   y[b,t,c] = act(bias[c] + sum_{j<K} w[c,j] * x[b, t - K + 1 + j, c])
+ * x [B,T,C] in_dtype (pitched) or [T,C] with cu; w [C,K] fp32 (w[c,K-1] weighs the token
+ * itself); bias [C] fp32, nullable; act: sdm_gate_act; y like x, contiguous.
+ * state [B,K-1,C] in_dtype, a sequence's last K - 1 inputs, oldest first: SDM_CONTINUE reads
+ * it as the inputs before the first token, SDM_INIT_ZERO takes those as zero (state may then
+ * be NULL: not kept); it is rewritten with the last K - 1 inputs seen (an empty sequence
+ * keeps its state, or gets zeros with SDM_INIT_ZERO).  One launch.
+ */
+sdm_status sdm_conv_forward(const void *x, const float *w, const float *bias, void *state,
+                            int32_t init, int32_t act, const int32_t *cu, void *y,
+                            sdm_conv_shape shape, void *stream);
+
+/* One token of each of B sequences: x, y [B,C]; state as above, read and moved up by one.
+ * shape.T is ignored.  The same results as sdm_conv_forward with T = 1 and SDM_CONTINUE. */
+sdm_status sdm_conv_step(const void *x, const float *w, const float *bias, void *state,
+                         int32_t act, void *y, sdm_conv_shape shape, void *stream);
+
+/* B sequences, T tokens (rows in all when packed), H heads in G groups that share k and q (H a
+ * multiple of G), N state rows per head and d_v values per row (multiples of 8, 8 to 256).
+ * in_dtype: element type of k, q, v, dt, gate and y.  softplus != 0: the step sizes are
+ * softplus(dt + dt_bias), else dt + dt_bias with negative values taken as 0. */
+typedef struct {
+    int32_t B, T, H, G, N, d_v;
+    int32_t in_dtype, softplus;
+    int64_t k_stride, q_stride, v_stride, dt_stride, gate_stride;
+} sdm_ssm_shape;
+
+/* Bytes of scratch that sdm_ssm_forward needs for this shape, packed or not; 0 for an invalid
+ * shape. */
+size_t sdm_ssm_workspace_size(sdm_ssm_shape shape);
+
+/*
+ * Selective state-space scan over T tokens.  Token t of sequence b, head h, g = h / (H / G):
+ *   d = softplus(dt[b,t,h] + dt_bias[h])
+ *   M[b,h] = exp(d * A[h]) * M[b,h] + d * k[b,t,g] (x) v[b,t,h]        (N x d_v)
+ *   y[b,t,h] = (q[b,t,g]^T M[b,h] + D[h] * v[b,t,h]) * act(gate[b,t,h])
+ *   k, q [B,T,G,N], v, gate [B,T,H,d_v], dt [B,T,H] in_dtype (pitched, or packed without B);
+ *   gate nullable (no factor); A [H] fp32, finite and <= 0; dt_bias, D [H] fp32, nullable (0);
+ *   M [B,H,N,d_v] fp32, the state: SDM_CONTINUE starts from it, SDM_INIT_ZERO from zero, and
+ *   it is left as it is after the last token; y [B,T,H,d_v] in_dtype, contiguous.
+ * ws / ws_bytes: at least sdm_ssm_workspace_size bytes, 256-byte aligned, NULL if that is 0;
+ * calls that overlap on the GPU need one each.
+ * k, q, v and dt have to be finite: a NaN or infinity also reaches other tokens of its sequence
+ * (never another sequence).
+ */
+sdm_status sdm_ssm_forward(const void *k, const void *q, const void *v, const void *dt,
+                           const float *A, const float *dt_bias, const float *D, float *M,
+                           int32_t init, const void *gate, int32_t act, const int32_t *cu,
+                           void *y, void *ws, size_t ws_bytes, sdm_ssm_shape shape,
+                           void *stream);
+
+/* One token of each of B sequences: k, q [B,G,N], v, gate, y [B,H,d_v], dt [B,H]; M is read and
+ * rewritten.  shape.T is ignored; no scratch.  The arithmetic of sdm_ssm_forward with T = 1
+ * and SDM_CONTINUE. */
+sdm_status sdm_ssm_step(const void *k, const void *q, const void *v, const void *dt,
+                        const float *A, const float *dt_bias, const float *D, float *M,
+                        const void *gate, int32_t act, void *y, sdm_ssm_shape shape,
+                        void *stream);
+
+/*
+ * The norms after and before a block, fused with the block's gate, its residual scale and the
+ * residual sum, for `rows` rows of D channels (a multiple of 8, 8 to 16384):
+ *   f = u * rsqrt(mean(u^2) + eps) * post_gamma     (post_norm != 0; else f = u)
+ *   f = f * act(gate) * scale                       (each factor only if not NULL)
+ *   r_out = r + f
+ *   n = r_out * rsqrt(mean(r_out^2) + eps) * pre_gamma     (of the unrounded r_out)
+ * u (the block's output), gate, n in in_dtype; r, r_out (the residual stream) in r_dtype;
+ * post_gamma, scale, pre_gamma [D] fp32, nullable (1); n nullable (not computed).  r_out may be
+ * r and n may be u or gate (the same pointer).  eps >= 0.  One launch.
+ */
+sdm_status sdm_block_norm(const void *u, const void *gate, int32_t act, int32_t post_norm,
+                          const float *post_gamma, const float *scale, const void *r,
+                          int32_t r_dtype, const float *pre_gamma, float eps, void *r_out,
+                          void *n, int64_t rows, int32_t D, int32_t in_dtype, void *stream);
+
 /* Kinds of kernel launch reported by the timing calls below. */
 typedef enum {
     SDM_KERNEL_STATE_INIT = 0, /* M0 broadcast into M                         */
@@ -333,6 +438,9 @@ typedef enum {
     SDM_KERNEL_STATE_ROWS = 7, /* state checkpoint pack / unpack              */
     SDM_KERNEL_UNDO = 8,       /* undo of a logged pass                       */
     SDM_KERNEL_SCAN_CHUNK = 9, /* steps 2-3, chunk-wise engine                */
+    SDM_KERNEL_CONV = 10,      /* short convolution, prompts and single tokens */
+    SDM_KERNEL_SSM = 11,       /* state-space scan, prompts and single tokens */
+    SDM_KERNEL_BLOCK_NORM = 12, /* norms around a block                       */
     SDM_KERNEL_KINDS = 16
 } sdm_kernel_kind;
 

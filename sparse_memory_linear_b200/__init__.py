@@ -13,10 +13,15 @@ from ._binding import (  # noqa: F401
     ROW_FORMAT,
     SDM_BF16,
     SDM_F32,
+    SdmConvShape,
     SdmError,
     SdmShape,
+    SdmSsmShape,
     library,
     library_path,
+    sdm_block_norm,
+    sdm_conv_forward,
+    sdm_conv_step,
     sdm_decode_step,
     sdm_decode_step_chained,
     sdm_decode_step_coupled,
@@ -34,6 +39,9 @@ from ._binding import (  # noqa: F401
     sdm_select,
     sdm_set_option,
     sdm_slot_cta_stats,
+    sdm_ssm_forward,
+    sdm_ssm_step,
+    sdm_ssm_workspace_size,
     sdm_state_init,
     sdm_state_pack,
     sdm_state_rows_bytes,

@@ -10,7 +10,7 @@ import torch
 
 SDM_F32, SDM_BF16 = 0, 1
 ENGINE = {"auto": 0, "seq": 1, "slot": 2, "chunk": 3}
-INIT = {"m0": 0, "continue": 1}
+INIT = {"m0": 0, "continue": 1, "zero": 2}
 ACT = {"silu": 0, "sigmoid": 1, "identity": 2}
 _STATUS = {0: "SDM_OK", 1: "SDM_ERR_INVALID_ARG", 2: "SDM_ERR_UNSUPPORTED", 3: "SDM_ERR_CUDA",
            4: "SDM_ERR_DEVICE_CHECK", 5: "SDM_ERR_TIMEOUT"}
@@ -25,6 +25,18 @@ class SdmShape(ctypes.Structure):
 
     def __repr__(self):
         return "SdmShape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class SdmConvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "C", "K", "in_dtype")] \
+        + [("x_stride", ctypes.c_int64)]
+
+
+class SdmSsmShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "H", "G", "N", "d_v", "in_dtype",
+                                               "softplus")] \
+        + [(n, ctypes.c_int64) for n in ("k_stride", "q_stride", "v_stride", "dt_stride",
+                                         "gate_stride")]
 
 
 class SdmError(RuntimeError):
@@ -47,7 +59,7 @@ def library():
             "`python -c 'import __graft_entry__ as g; g.build()'` (nvcc, sm_100a)")
     lib = ctypes.CDLL(library_path)
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
-    S = SdmShape
+    S, CS, SS, L = SdmShape, SdmConvShape, SdmSsmShape, ctypes.c_int64
     sig = {
         "sdm_select": ([P, S, I, P, P, P], I),
         "sdm_workspace_size": ([S, I], Z),
@@ -76,6 +88,12 @@ def library():
         "sdm_state_rows_bytes": ([ctypes.c_int64, I, I], Z),
         "sdm_state_pack": ([P, ctypes.c_int64, I, I, P, P, P], I),
         "sdm_state_unpack": ([P, P, ctypes.c_int64, I, I, P, P], I),
+        "sdm_conv_forward": ([P, P, P, P, I, I, P, P, CS, P], I),
+        "sdm_conv_step": ([P, P, P, P, I, P, CS, P], I),
+        "sdm_ssm_workspace_size": ([SS], Z),
+        "sdm_ssm_forward": ([P, P, P, P, P, P, P, P, I, P, I, P, P, P, Z, SS, P], I),
+        "sdm_ssm_step": ([P, P, P, P, P, P, P, P, P, I, P, SS, P], I),
+        "sdm_block_norm": ([P, P, I, I, P, P, P, I, P, F, P, P, L, I, I, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -476,8 +494,255 @@ def sdm_state_unpack(codes, scales, d_v: int, fmt: str = "e4m3", *, out=None, st
     return out
 
 
+# ------------------------------------------------------------------ the dense-state layer
+_DTYPES = {torch.float32: SDM_F32, torch.bfloat16: SDM_BF16}
+
+
+def _on_device(dev):
+    """The library launches on the calling thread's current device: a guard that makes it
+    the tensors' (None where it is already)."""
+    return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _call(name, dev, stream, *args):
+    """Calls the entry point with the stream as its last argument, on the tensors' device."""
+    fn = getattr(_lib or library(), name)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    guard = _on_device(dev)
+    if guard is None:
+        rc = fn(*args, int(stream))
+    else:
+        with guard:
+            rc = fn(*args, int(stream))
+    if rc != 0:
+        raise SdmError(rc, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _param(t, name, shape, dev):
+    """The address of a contiguous fp32 parameter (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _expect(t, name, shape)
+        _need(t, name, torch.float32, dev)
+    return t.data_ptr()
+
+
+def _like(t, name, shape, dtype, dev):
+    """Checks a contiguous tensor of the call's shape, type and device (None passes)."""
+    if t is not None and (t.dtype != dtype or t.shape != shape or t.device != dev
+                          or not t.is_contiguous()):
+        _expect(t, name, shape)
+        _need(t, name, dtype, dev)
+    return t
+
+
+def _pitch(t, name, shape, lead, dtype, dev):
+    """The distance in elements between the rows of consecutive tokens of a tensor [*lead, ...]
+    whose rows are contiguous; the rows of the next sequence follow at the same distance."""
+    if t.shape != shape:
+        _expect(t, name, shape)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.is_contiguous():
+        return 0
+    st = t.stride()
+    width = 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and st[i] != width:
+            raise ValueError(f"{name}: a token's values must be contiguous")
+        width *= shape[i]
+    pitch, rows = 0, 1
+    for i in range(lead - 1, -1, -1):
+        if shape[i] == 1:
+            continue
+        if pitch == 0:
+            pitch = st[i]
+        elif st[i] != rows * pitch:
+            raise ValueError(f"{name}: the rows of its sequences must follow one another")
+        rows *= shape[i]
+    if rows > 1 and pitch < width:
+        raise ValueError(f"{name}: rows overlap")
+    return pitch if rows > 1 else 0
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"inputs must be bfloat16 or float32, got {t.dtype}")
+    return t.device, t.dtype
+
+
+def _dense_init(init):
+    if init not in ("zero", "continue"):
+        raise ValueError(f"init must be 'zero' or 'continue', got {init!r}")
+    return INIT[init]
+
+
+def _batch(cu, lead, dev):
+    """(B, T) of a batch: [B, T] rows, or [T] packed rows with cu [B + 1]."""
+    if cu is None:
+        if len(lead) != 2:
+            raise ValueError(f"expected [B, T, ...] rows, got {len(lead)} leading dimensions")
+        return lead
+    if len(lead) != 1:
+        raise ValueError(f"expected packed [T, ...] rows with cu, got {len(lead)} leading "
+                         "dimensions")
+    if cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError(f"cu has shape {tuple(cu.shape)}, expected [B + 1]")
+    _need(cu, "cu", torch.int32, dev)
+    return cu.shape[0] - 1, lead[0]
+
+
+def sdm_conv_forward(x, w, state=None, *, bias=None, init: str = "zero", act: str = "silu",
+                     cu=None, y=None, stream=None):
+    """Causal short convolution over the channels of x [B,T,C] (or packed [T,C] with cu int32
+    [B+1]; rows may be pitched).  w [C,K] fp32, K = 2 to 4, bias [C] fp32; state [B,K-1,C]
+    (a sequence's last K-1 inputs) is read with init="continue" and rewritten.  Returns y."""
+    dev, dt = _cuda(x, "x")
+    B, T = _batch(cu, tuple(x.shape[:-1]), dev)
+    C = x.shape[-1]
+    if w.dim() != 2:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected [C, K]")
+    K = w.shape[1]
+    pitch = _pitch(x, "x", x.shape, x.dim() - 1, dt, dev)
+    if y is None:
+        y = torch.empty(x.shape, dtype=dt, device=dev)
+    else:
+        _like(y, "y", x.shape, dt, dev)
+    _like(state, "state", (B, K - 1, C), dt, dev)
+    _call("sdm_conv_forward", dev, stream, x.data_ptr(), _param(w, "w", (C, K), dev),
+          _param(bias, "bias", (C,), dev), _addr(state), _dense_init(init), ACT[act], _addr(cu),
+          y.data_ptr(), SdmConvShape(B, T, C, K, _DTYPES[dt], pitch))
+    return y
+
+
+def sdm_conv_step(x, w, state, *, bias=None, act: str = "silu", y=None, stream=None):
+    """One token of each sequence: x [B,C] (rows may be pitched), w [C,K] fp32, bias [C] fp32;
+    state [B,K-1,C] is read and moved up by one.  Returns y [B,C]."""
+    dev, dt = _cuda(x, "x")
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"x and w must be [B, C] and [C, K], got {tuple(x.shape)} and "
+                         f"{tuple(w.shape)}")
+    B, C = x.shape
+    K = w.shape[1]
+    pitch = _pitch(x, "x", x.shape, 1, dt, dev)
+    if y is None:
+        y = torch.empty(x.shape, dtype=dt, device=dev)
+    else:
+        _like(y, "y", x.shape, dt, dev)
+    _like(state, "state", (B, K - 1, C), dt, dev)
+    _call("sdm_conv_step", dev, stream, x.data_ptr(), _param(w, "w", (C, K), dev),
+          _param(bias, "bias", (C,), dev), state.data_ptr(), ACT[act], y.data_ptr(),
+          SdmConvShape(B, 1, C, K, _DTYPES[dt], pitch))
+    return y
+
+
+def _ssm_shape(k, q, v, dt, A, M, D, dt_bias, gate, y, softplus, B, T, dev, dtype):
+    """Checks the arguments that both forms share; returns (shape, y, parameter addresses)."""
+    lead = tuple(v.shape[:-2])
+    nl = len(lead)
+    H, P = v.shape[-2:]
+    G, N = k.shape[-2:]
+    kshape = lead + (G, N)
+    shape = SdmSsmShape(
+        B, T, H, G, N, P, _DTYPES[dtype], 1 if softplus else 0,
+        _pitch(k, "k", kshape, nl, dtype, dev), _pitch(q, "q", kshape, nl, dtype, dev),
+        _pitch(v, "v", v.shape, nl, dtype, dev), _pitch(dt, "dt", lead + (H,), nl, dtype, dev),
+        _pitch(gate, "gate", v.shape, nl, dtype, dev) if gate is not None else 0)
+    _like(M, "M", (B, H, N, P), torch.float32, dev)
+    params = (_param(A, "A", (H,), dev), _param(dt_bias, "dt_bias", (H,), dev),
+              _param(D, "D", (H,), dev))
+    if y is None:
+        y = torch.empty(v.shape, dtype=dtype, device=dev)
+    else:
+        _like(y, "y", v.shape, dtype, dev)
+    return shape, y, params
+
+
+def sdm_ssm_workspace_size(shape: SdmSsmShape) -> int:
+    return int(library().sdm_ssm_workspace_size(shape))
+
+
+def sdm_ssm_forward(k, q, v, dt, A, M, *, init: str = "zero", D=None, dt_bias=None,
+                    softplus: bool = True, gate=None, act: str = "silu", cu=None, y=None,
+                    ws=None, stream=None):
+    """Selective state-space scan.  k, q [B,T,G,N], v, gate [B,T,H,d_v], dt [B,T,H] in one type
+    (or packed, without B, with cu int32 [B+1]; rows may be pitched: slices of one projected
+    row); A [H] fp32 (<= 0), D, dt_bias [H] fp32; M [B,H,N,d_v] fp32, read with
+    init="continue" and left as it is after the last token.  Returns y like v."""
+    dev, dtype = _cuda(v, "v")
+    if v.dim() < 3 or k.dim() != v.dim():
+        raise ValueError(f"k and v must be [..., G, N] and [..., H, d_v] rows, got "
+                         f"{tuple(k.shape)} and {tuple(v.shape)}")
+    B, T = _batch(cu, tuple(v.shape[:-2]), dev)
+    shape, y, params = _ssm_shape(k, q, v, dt, A, M, D, dt_bias, gate, y, softplus, B, T, dev,
+                                  dtype)
+    if ws is None:
+        ws = torch.empty(max(sdm_ssm_workspace_size(shape), 1), dtype=torch.uint8, device=dev)
+    _need(ws, "ws", torch.uint8, dev)
+    _call("sdm_ssm_forward", dev, stream, k.data_ptr(), q.data_ptr(), v.data_ptr(),
+          dt.data_ptr(), *params, M.data_ptr(), _dense_init(init), _addr(gate), ACT[act],
+          _addr(cu), y.data_ptr(), ws.data_ptr(), ws.numel(), shape)
+    return y
+
+
+def sdm_ssm_step(k, q, v, dt, A, M, *, D=None, dt_bias=None, softplus: bool = True, gate=None,
+                 act: str = "silu", y=None, stream=None):
+    """One token of each sequence: k, q [B,G,N], v, gate [B,H,d_v], dt [B,H]; M [B,H,N,d_v]
+    fp32 is read and rewritten.  Returns y [B,H,d_v]."""
+    dev, dtype = _cuda(v, "v")
+    if v.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"k and v must be [B, G, N] and [B, H, d_v], got {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    shape, y, params = _ssm_shape(k, q, v, dt, A, M, D, dt_bias, gate, y, softplus, v.shape[0],
+                                  1, dev, dtype)
+    _call("sdm_ssm_step", dev, stream, k.data_ptr(), q.data_ptr(), v.data_ptr(), dt.data_ptr(),
+          *params, M.data_ptr(), _addr(gate), ACT[act], y.data_ptr(), shape)
+    return y
+
+
+def sdm_block_norm(u, r, *, post_norm: bool = True, post_gamma=None, gate=None,
+                   act: str = "silu", scale=None, pre_gamma=None, eps: float = 1e-6,
+                   r_out=None, n=None, want_n: bool = True, stream=None):
+    """The norms after and before a block: with f = norm(u) * post_gamma (post_norm) * act(gate)
+    * scale, returns (r + f, norm(r + f) * pre_gamma).  u, gate [..., D] in one type, r [..., D]
+    the residual stream (bf16 or fp32); post_gamma, scale, pre_gamma [D] fp32.  r_out may be
+    r, n may be u or gate.  want_n=False: the second result is None."""
+    dev, dtype = _cuda(u, "u")
+    _, rdt = _cuda(r, "r")
+    D = u.shape[-1]
+    _like(u, "u", u.shape, dtype, dev)
+    _like(r, "r", u.shape, rdt, dev)
+    _like(gate, "gate", u.shape, dtype, dev)
+    if r_out is None:
+        r_out = torch.empty(u.shape, dtype=rdt, device=dev)
+    else:
+        _like(r_out, "r_out", u.shape, rdt, dev)
+    if n is None:
+        n = torch.empty(u.shape, dtype=dtype, device=dev) if want_n else None
+    else:
+        _like(n, "n", u.shape, dtype, dev)
+    _call("sdm_block_norm", dev, stream, u.data_ptr(), _addr(gate), ACT[act],
+          1 if post_norm else 0, _param(post_gamma, "post_gamma", (D,), dev),
+          _param(scale, "scale", (D,), dev), r.data_ptr(), _DTYPES[rdt],
+          _param(pre_gamma, "pre_gamma", (D,), dev), eps, r_out.data_ptr(), _addr(n),
+          u.numel() // D if D else 0, D, _DTYPES[dtype])
+    return r_out, n
+
+
 KERNEL_KINDS = ("state_init", "select", "scan_seq", "scan_slot", "norm_gate", "decode",
-                "slot_sort", "state_rows", "undo", "scan_chunk")
+                "slot_sort", "state_rows", "undo", "scan_chunk", "conv", "ssm", "block_norm")
 
 
 def sdm_profile_enable(on: bool = True):

@@ -1,0 +1,262 @@
+// conv.cuh -- causal short convolution over the channels of a recurrent layer (prompts and
+// single tokens).
+//
+// y[t, c] = act(bias[c] + sum_j w[c, j] x[t - K + 1 + j, c]), j = 0..K-1, each channel on its
+// own; inputs before a sequence's first token are the kept state (its last K - 1 inputs) or
+// zero.
+#pragma once
+
+#include "common.cuh"
+
+namespace sdm {
+
+// Eight values of a 16-bit or 32-bit row: 16 or 32 bytes.
+template <typename T>
+struct Vec8;
+
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 raw;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    raw = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = raw;
+  }
+  __device__ __forceinline__ void zero() { raw = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float f[8]) const {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 t = __bfloat1622float2(h[j]);
+      f[2 * j] = t.x;
+      f[2 * j + 1] = t.y;
+    }
+  }
+  __device__ __forceinline__ void set(const float f[8]) {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+  }
+};
+
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float f[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float f[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// Row bounds of the sequences of a batch: B sequences of T rows each (cu == nullptr), or
+// packed, sequence b holding rows cu[b] .. cu[b + 1] - 1 of R.  Offsets are clamped to [0, R]
+// and an end below its start gives an empty sequence, so that no bad offset leaves the buffers.
+struct SeqBounds {
+  const int* cu;
+  int B;
+  long long T;  // uniform length (cu == nullptr)
+  long long R;  // rows in all
+
+  __device__ __forceinline__ long long start(int b) const {
+    if (!cu) return (long long)b * T;
+    const long long s = cu[b];
+    return s < 0 ? 0 : s > R ? R : s;
+  }
+  __device__ __forceinline__ long long end(int b) const {
+    if (!cu) return (long long)(b + 1) * T;
+    const long long s = start(b), e = start(b + 1);
+    return e < s ? s : e;
+  }
+  // The first sequence that starts at row r or later (B: none).
+  __device__ __forceinline__ int first_from(long long r) const {
+    if (!cu) {
+      const long long b = (r + T - 1) / T;
+      return b > B ? B : (int)b;
+    }
+    int lo = 0, hi = B;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (start(mid) < r) lo = mid + 1; else hi = mid;
+    }
+    return lo;
+  }
+  // Records offsets that are out of range or not ascending; called by one block.
+  __device__ __forceinline__ void check() const {
+    if (!cu) return;
+    for (int b = threadIdx.x; b <= B; b += blockDim.x) {
+      const int c = cu[b];
+      if (c < 0 || c > R || (b > 0 && c < cu[b - 1])) record_status(STATUS_BAD_INDEX);
+    }
+  }
+};
+
+struct ConvArgs {
+  const void* x;
+  const float* w;
+  const float* bias;
+  void* state;  // [B, K - 1, C]; may be null when from_zero
+  void* y;
+  SeqBounds seq;
+  int C, cv;  // channels, C / 8
+  int from_zero, act, rows_per_thread;
+  long long x_stride, tiles;
+};
+
+template <typename T, int K>
+struct ConvWeights {
+  float w[K][8], bias[8];
+  __device__ __forceinline__ void load(const float* wp, const float* bp, int c0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) w[j][e] = __ldg(wp + (size_t)(c0 + e) * K + j);
+      bias[e] = bp ? __ldg(bp + c0 + e) : 0.0f;
+    }
+  }
+  // One output row from its K input rows (oldest first).
+  __device__ __forceinline__ void row(const Vec8<T> in[K], int act, T* out) const {
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = bias[e];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      float f[8];
+      in[j].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j][e], f[e], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = gate_act(acc[e], act);
+    Vec8<T> o;
+    o.set(acc);
+    o.store(out);
+  }
+};
+
+// One thread walks `rows_per_thread` rows of eight channels with the last K - 1 inputs in
+// registers.  The first K - 1 rows of a sequence need its kept state, and the state is
+// rewritten in place; so the thread whose rows hold a sequence's first row also computes the
+// rest of those K - 1 rows and writes the new state, and no other thread touches the state.
+template <typename T, int K>
+__global__ void __launch_bounds__(256) conv_forward_kernel(ConvArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (blockIdx.x == 0) a.seq.check();
+  const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long tile = idx / a.cv;
+  if (tile >= a.tiles) return;
+  const int c0 = (int)(idx - tile * a.cv) * 8;
+  const T* x = static_cast<const T*>(a.x) + c0;
+  T* y = static_cast<T*>(a.y) + c0;
+  T* state = a.state ? static_cast<T*>(a.state) + c0 : nullptr;
+  ConvWeights<T, K> cw;
+  cw.load(a.w, a.bias, c0);
+  const long long r0 = tile * a.rows_per_thread;
+  const bool last_tile = tile == a.tiles - 1;
+  const long long r1 = last_tile ? a.seq.R : r0 + a.rows_per_thread;
+
+  auto walk = [&](long long r, long long end, Vec8<T> win[K]) {
+    // win[0..K-2]: the K - 1 rows before r
+    for (; r + 4 <= end; r += 4) {
+      Vec8<T> nx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) nx[i].load(x + (r + i) * a.x_stride);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        win[K - 1] = nx[i];
+        cw.row(win, a.act, y + (r + i) * a.C);
+#pragma unroll
+        for (int j = 0; j + 1 < K; ++j) win[j] = win[j + 1];
+      }
+    }
+    for (; r < end; ++r) {
+      win[K - 1].load(x + r * a.x_stride);
+      cw.row(win, a.act, y + r * a.C);
+#pragma unroll
+      for (int j = 0; j + 1 < K; ++j) win[j] = win[j + 1];
+    }
+  };
+
+  int b = a.seq.first_from(r0);
+  if (b > 0) {  // the sequence that runs on from an earlier thread's rows
+    const long long s0 = a.seq.start(b - 1), e0 = a.seq.end(b - 1);
+    long long r = s0 + K - 1 > r0 ? s0 + K - 1 : r0;
+    const long long end = e0 < r1 ? e0 : r1;
+    if (s0 < r0 && r < end) {
+      Vec8<T> win[K];
+#pragma unroll
+      for (int j = 0; j + 1 < K; ++j) win[j].load(x + (r - (K - 1) + j) * a.x_stride);
+      walk(r, end, win);
+    }
+  }
+  for (; b < a.seq.B; ++b) {
+    const long long s0 = a.seq.start(b), e0 = a.seq.end(b);
+    if (s0 >= r1 && !last_tile) break;
+    Vec8<T> win[K];
+#pragma unroll
+    for (int j = 0; j + 1 < K; ++j) {
+      if (a.from_zero)
+        win[j].zero();
+      else
+        win[j].load(state + ((size_t)b * (K - 1) + j) * a.C);
+    }
+    if (state) {  // the sequence's last K - 1 inputs, older ones from the kept state
+#pragma unroll
+      for (int j = 0; j + 1 < K; ++j) {
+        const long long r = e0 - (K - 1) + j;
+        Vec8<T> t;
+        if (r >= s0) {
+          t.load(x + r * a.x_stride);
+        } else {
+          const long long o = r - s0 + (K - 1);  // index among the kept inputs, 0..K-2
+          t = win[0];
+#pragma unroll
+          for (int i = 1; i + 1 < K; ++i)
+            if (o == i) t = win[i];
+        }
+        t.store(state + ((size_t)b * (K - 1) + j) * a.C);
+      }
+    }
+    long long end = s0 + K - 1 > r1 ? s0 + K - 1 : r1;
+    if (e0 < end) end = e0;
+    walk(s0, end, win);
+  }
+}
+
+// One token: the state's K - 1 inputs and the new one give the output, and the state moves up
+// by one.  A thread per eight channels of a sequence.
+template <typename T, int K>
+__global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long b = idx / a.cv;
+  if (b >= a.seq.B) return;
+  const int c0 = (int)(idx - b * a.cv) * 8;
+  T* state = static_cast<T*>(a.state) + (size_t)b * (K - 1) * a.C + c0;
+  Vec8<T> win[K];
+#pragma unroll
+  for (int j = 0; j + 1 < K; ++j) win[j].load(state + (size_t)j * a.C);
+  win[K - 1].load(static_cast<const T*>(a.x) + b * a.x_stride + c0);
+  ConvWeights<T, K> cw;
+  cw.load(a.w, a.bias, c0);
+#pragma unroll
+  for (int j = 0; j + 1 < K; ++j) win[j + 1].store(state + (size_t)j * a.C);
+  cw.row(win, a.act, static_cast<T*>(a.y) + (size_t)b * a.C + c0);
+}
+
+}  // namespace sdm

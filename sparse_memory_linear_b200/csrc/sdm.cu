@@ -5,13 +5,16 @@
 
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "block_norm.cuh"
 #include "common.cuh"
+#include "conv.cuh"
 #include "decode.cuh"
 #include "norm_init.cuh"
 #include "rows.cuh"
@@ -21,6 +24,7 @@
 #include "scan_slot.cuh"
 #include "select.cuh"
 #include "select_fast.cuh"
+#include "ssm.cuh"
 
 using namespace sdm;
 
@@ -1427,3 +1431,5 @@ extern "C" sdm_status sdm_scan_forward_noalloc(const void* kp, const void* qp, c
                           sel_out, SDM_ENGINE_SEQ, ws, SDM_NOALLOC_SCRATCH_BYTES, shape,
                           stream);
 }
+
+#include "dense_api.cuh"
