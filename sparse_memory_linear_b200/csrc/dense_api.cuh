@@ -175,6 +175,68 @@ cudaError_t launch_ssm_scan(const SsmArgs& a, dim3 grid, cudaStream_t st) {
   return launch_pdl<true>(ssm_scan_kernel<T, 8>, grid, block, 0, st, a);
 }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor map encoder, looked up once per process.
+EncodeTiledFn tensor_map_encoder() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// Rows of `heads` x `width` bf16 values at a pitch, read in tiles of 128 rows x 64 values of one
+// head, with zeros where the head or the rows end.
+bool tile_map(CUtensorMap* map, const void* p, int width, int heads, long long rows,
+              long long pitch) {
+  const EncodeTiledFn encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)pitch * 2};
+  const cuuint32_t box[3] = {64, 1, SB_L}, steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box,
+                steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The block-wise scan's shapes: bf16, at most 128 state rows, and prompts long enough to fill
+// a part of a block.
+bool ssm_block_fits(const sdm_ssm_shape& s, long long R) {
+  return s.in_dtype == SDM_BF16 && s.N <= 128 && s.T >= 16 && R < 2147483647LL;
+}
+
+sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, cudaStream_t st) {
+  DeviceInfo* di;
+  const sdm_status rc = device_info(&di);
+  if (rc != SDM_OK) return rc;
+  SsmBlockArgs ba;
+  ba.a = a;
+  ba.seg_blocks = 1 << 24;
+  ba.ptiles = (s.d_v + SB_P - 1) / SB_P;
+  if (!tile_map(&ba.mq, a.q, s.N, s.G, a.seq.R, a.q_stride) ||
+      !tile_map(&ba.mk, a.k, s.N, s.G, a.seq.R, a.k_stride) ||
+      !tile_map(&ba.mv, a.v, s.d_v, s.H, a.seq.R, a.v_stride))
+    return SDM_ERR_CUDA;
+  const long long items = s.B, blocks = items * s.H * ba.ptiles;
+  if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;
+  SDM_CUDA_TRY(launch_pdl(ssm_block_kernel, dim3((unsigned)blocks), dim3(SB_THREADS),
+                          (size_t)SB_SMEM, st, ba));
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return SDM_OK;
+}
+
 template <typename T, typename TR>
 cudaError_t launch_block_norm(const BlockNormArgs& a, const DeviceInfo* di, cudaStream_t st) {
   const int nvec = a.D / 8;
@@ -242,6 +304,7 @@ sdm_status sdm_ssm_forward(const void* k, const void* q, const void* v, const vo
   a.seq = SeqBounds{cu, s.B, s.T, R};
   a.from_zero = init == SDM_INIT_ZERO;
   ProfScope ps(SDM_KERNEL_SSM, st);
+  if (ssm_block_fits(s, R)) return ssm_block_run(s, a, st);
   const dim3 grid((unsigned)s.B, (unsigned)s.H, (unsigned)((s.d_v + SSM_COLS - 1) / SSM_COLS));
   if (s.in_dtype == SDM_BF16)
     SDM_CUDA_TRY(launch_ssm_scan<__nv_bfloat16>(a, grid, st));

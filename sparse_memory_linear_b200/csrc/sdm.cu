@@ -25,6 +25,7 @@
 #include "select.cuh"
 #include "select_fast.cuh"
 #include "ssm.cuh"
+#include "ssm_block.cuh"
 
 using namespace sdm;
 
@@ -146,6 +147,9 @@ sdm_status device_info(DeviceInfo** out) {
   SDM_CUDA_TRY(allow_max_dynamic_smem(slot_chunk_kernel<NQ, G, PF, true>, m));
     SDM_SLOT_ATTR(1, 4, 6) SDM_SLOT_ATTR(2, 2, 6) SDM_SLOT_ATTR(4, 4, 4) SDM_SLOT_ATTR(8, 2, 2)
 #undef SDM_SLOT_ATTR
+    SDM_CUDA_TRY(cudaFuncSetAttribute(ssm_block_kernel,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)SB_SMEM));
     d.attrs_set = true;
   }
   *out = &d;
