@@ -196,15 +196,15 @@ EncodeTiledFn tensor_map_encoder() {
   return fn;
 }
 
-// Rows of `heads` x `width` bf16 values at a pitch, read in tiles of 128 rows x 64 values of one
-// head, with zeros where the head or the rows end.
+// Rows of `heads` x `width` bf16 values at a pitch, moved in tiles of `box_rows` rows x 64 values
+// of one head; loads give zeros where the head or the rows end, stores stop there.
 bool tile_map(CUtensorMap* map, const void* p, int width, int heads, long long rows,
-              long long pitch) {
+              long long pitch, int box_rows) {
   const EncodeTiledFn encode = tensor_map_encoder();
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)pitch * 2};
-  const cuuint32_t box[3] = {64, 1, SB_L}, steps[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, steps[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box,
                 steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -225,9 +225,10 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, cudaStream_t 
   ba.a = a;
   ba.seg_blocks = 1 << 24;
   ba.ptiles = (s.d_v + SB_P - 1) / SB_P;
-  if (!tile_map(&ba.mq, a.q, s.N, s.G, a.seq.R, a.q_stride) ||
-      !tile_map(&ba.mk, a.k, s.N, s.G, a.seq.R, a.k_stride) ||
-      !tile_map(&ba.mv, a.v, s.d_v, s.H, a.seq.R, a.v_stride))
+  if (!tile_map(&ba.mq, a.q, s.N, s.G, a.seq.R, a.q_stride, SB_L) ||
+      !tile_map(&ba.mk, a.k, s.N, s.G, a.seq.R, a.k_stride, SB_L) ||
+      !tile_map(&ba.mv, a.v, s.d_v, s.H, a.seq.R, a.v_stride, SB_L) ||
+      !tile_map(&ba.my, a.y, s.d_v, s.H, a.seq.R, (long long)s.H * s.d_v, 32))
     return SDM_ERR_CUDA;
   const long long items = s.B, blocks = items * s.H * ba.ptiles;
   if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;

@@ -6,9 +6,11 @@
 //   M'  = exp(c_L) M + sum_s exp(c_L - c_s) d_s k_s (x) v_s
 // so a block is four matrix products, all on tcgen05 with fp32 sums in tensor memory:
 //   S  = q k^T                      128 x 128 x N
-//   Y2 = q M                        128 x 64 x N, M as two bf16 parts (16 bits of it)
+//   Y2 = q M                        128 x (2 x 64) x N, M as two bf16 parts (16 bits of it)
 //   Y1 = (S o weights) v            128 x 64 x 128, weights rounded to bf16
-//   dM = k^T (w o v)                N x 64 x 128, w o v as three bf16 parts (24 bits)
+//   dM = k^T (w o v)                N x (3 x 64) x 128, w o v as three bf16 parts (24 bits)
+// The parts lie side by side as columns of one product, so that q and k are read from shared
+// memory once for all of them: its bandwidth is what the matrix unit waits for at these sizes.
 // The state is kept in fp32 registers and never rounded to less: dM has to be exact to fp32,
 // hence the three parts.  What enters y may be rounded to the type of y once: each token's
 // weight in another's read (half a step of bf16); two parts of M keep the second term below
@@ -17,11 +19,12 @@
 // One CTA walks the blocks of (sequence segment, head, 64 value columns) in order:
 //   warps 0-3    a thread per token row: weighs S into P (tensor memory), then joins
 //                y = exp(c_t) Y2 + Y1 + D v, gates and stores it
-//   warps 4-7    a thread per state row, and quarter rows of v: w o v in parts, state update
-//   warp 8       issues S, Y2, Y1        warp 9   issues dM
-//   warp 10      TMA loads of q, k, v    warp 11  step sizes and decay sums, a block ahead
-// joined by mbarriers; block c + 1's S is weighed before block c's y is joined, so the matrix
-// unit and both groups of warps work at once.
+//   warps 4-7    a thread per state row: adds dM to the decayed state, publishes its two parts
+//   warps 8-11   a thread per quarter row of v: w o v in parts
+//   warp 12      issues S, Y1            warp 13  issues dM
+//   warp 14      TMA loads of q, k, v    warp 15  step sizes and decay sums, two blocks ahead;
+//                                                 issues Y2
+// joined by mbarriers.
 //
 // Decays are summed within runs of 32 tokens (a warp's rows) and the runs' totals added, never as
 // differences of long sums: exp(c_t - c_s) is one exponential inside a run, and the product of
@@ -36,7 +39,7 @@ namespace sdm {
 
 constexpr int SB_L = 128;      // tokens of a block
 constexpr int SB_P = 64;       // value columns of a CTA
-constexpr int SB_THREADS = 384;
+constexpr int SB_THREADS = 512;
 
 // Shared memory, from a 1024-byte boundary.
 constexpr uint32_t SB_PANEL = 16384;                       // 128 rows of 128 bytes
@@ -58,23 +61,23 @@ struct SsmPrep {
 constexpr uint32_t SB_BARS = SB_PREP + 2 * sizeof(SsmPrep);
 enum {
   BAR_QFULL = 0, BAR_QFREE = 2, BAR_KFULL = 4, BAR_KFREE = 6, BAR_VFULL = 8, BAR_VFREE = 10,
-  BAR_PREP = 12, BAR_PREPFREE = 14, BAR_S = 16, BAR_P = 18, BAR_WREADY = 20, BAR_WFREE = 22,
-  BAR_CLEAN = 24, BAR_DRAIN = 26, BAR_DM = 28, BAR_HREADY, BAR_HFREE, BAR_Y, BAR_YFREE,
-  BAR_COUNT
+  BAR_PREP = 12, BAR_PREPFREE = 14, BAR_WREADY = 16, BAR_WFREE = 18, BAR_CLEAN = 20,
+  BAR_S = 22, BAR_P, BAR_Y, BAR_Y2, BAR_Y2FREE, BAR_DM, BAR_DMFREE, BAR_HREADY, BAR_HFREE,
+  BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 3
 };
 constexpr uint32_t SB_TMEM_PTR = SB_BARS + 40 * 8;
 static_assert(BAR_COUNT <= 40, "barriers");
 constexpr uint32_t SB_SMEM = SB_TMEM_PTR + 32 + 1024;      // and room to align
-static_assert(SB_SMEM <= 232448, "shared memory of a block");
+static_assert(SB_SMEM <= 232448 - 64, "shared memory of a block");
 
-// Tensor memory columns.
-constexpr uint32_t TM_S = 0, TM_Y1 = 256, TM_Y2 = 320, TM_DM = 448;
+// Tensor memory columns; P takes the first half of S's.
+constexpr uint32_t TM_S = 0, TM_Y1 = 128, TM_Y2 = 192, TM_DM = 320;
 
 constexpr float SB_LOG2E = 1.4426950408889634f;
 
 struct SsmBlockArgs {
   SsmArgs a;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, my;
   int seg_blocks;   // blocks of a segment
   int ptiles;       // 64-column tiles of d_v
 };
@@ -167,25 +170,27 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(BAR_QFULL + i), 1);
-      mbar_init(bar(BAR_QFREE + i), 1);
+      mbar_init(bar(BAR_QFREE + i), 2);
       mbar_init(bar(BAR_KFULL + i), 1);
       mbar_init(bar(BAR_KFREE + i), 2);
       mbar_init(bar(BAR_VFULL + i), 1);
       mbar_init(bar(BAR_VFREE + i), 4);
       mbar_init(bar(BAR_PREP + i), 1);
-      mbar_init(bar(BAR_PREPFREE + i), 8);
-      mbar_init(bar(BAR_S + i), 1);
-      mbar_init(bar(BAR_P + i), 4);
+      mbar_init(bar(BAR_PREPFREE + i), 12);
       mbar_init(bar(BAR_WREADY + i), 4);
       mbar_init(bar(BAR_WFREE + i), 1);
-      mbar_init(bar(BAR_DRAIN + i), 1);
       mbar_init(bar(BAR_CLEAN + i), 4);
     }
+    mbar_init(bar(BAR_S), 1);
+    mbar_init(bar(BAR_P), 4);
+    mbar_init(bar(BAR_Y), 1);
+    mbar_init(bar(BAR_Y2), 1);
+    mbar_init(bar(BAR_Y2FREE), 4);
     mbar_init(bar(BAR_DM), 1);
+    mbar_init(bar(BAR_DMFREE), 4);
     mbar_init(bar(BAR_HREADY), 4);
     mbar_init(bar(BAR_HFREE), 1);
-    mbar_init(bar(BAR_Y), 1);
-    mbar_init(bar(BAR_YFREE), 4);
+    for (int i = 0; i < 3; ++i) mbar_init(bar(BAR_DRAIN + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (npanels == 1) {  // state rows 64 and up: k is 0 there
@@ -217,134 +222,140 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     __nv_bfloat16* const yp = static_cast<__nv_bfloat16*>(a.y) + (size_t)h * a.P + p0;
     const __nv_bfloat16* const zp =
         a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)h * a.P + p0 : nullptr;
-    float f_prev = 0.0f;
-    for (int c = 0; c <= nb; ++c) {
-      float f_cur = 0.0f;
-      if (c < nb) {
-        if (!wait(BAR_PREP + (c & 1), c >> 1) || !wait(BAR_S + (c & 1), c >> 1)) break;
-        tc_fence_after();
-        const SsmPrep& pr = *prep(c);
-        const float in_t = pr.in[t];
-        // decay from the end of each earlier run up to t
-        float to[4];
-        {
-          float e = in_t;
+    for (int c = 0; c < nb; ++c) {
+      if (!wait(BAR_PREP + (c & 1), c >> 1) || !wait(BAR_S, c)) break;
+      tc_fence_after();
+      float decay;  // from the block's start up to t
+      const SsmPrep& pr = *prep(c);
+      const float in_t = pr.in[t];
+      // decay from the end of each earlier run up to t
+      float to[4];
+      {
+        float e = in_t;
 #pragma unroll
-          for (int j = 3; j >= 0; --j) {
-            to[j] = 0.0f;
-            if (j < warp) {
-              to[j] = exp2f(e);
-              e += pr.run[j];
-            }
+        for (int j = 3; j >= 0; --j) {
+          to[j] = 0.0f;
+          if (j < warp) {
+            to[j] = fast_exp2(e);
+            e += pr.run[j];
           }
-          f_cur = exp2f(e);
         }
-        const uint32_t sbuf = tm + TM_S + (uint32_t)(c & 1) * 128 + lanes;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t pk[16];
-          if (j > warp) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = 0u;
-          } else {
-            float s[32];
-            tmem_ld32(sbuf + 32 * j, s);
-            tmem_wait_ld();
-            if (j < warp) {
-              const float2 f2 = make_float2(to[j], to[j]);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 o = *reinterpret_cast<const float4*>(&pr.out[32 * j + 4 * i]);
-                const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
-                                      make_float2(s[4 * i], s[4 * i + 1]));
-                const float2 v = mul2(mul2(make_float2(o.z, o.w), f2),
-                                      make_float2(s[4 * i + 2], s[4 * i + 3]));
-                pk[2 * i] = pack_bf16(u.x, u.y);
-                pk[2 * i + 1] = pack_bf16(v.x, v.y);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 in = *reinterpret_cast<const float4*>(&pr.in[32 * j + 4 * i]);
-                const float4 d = *reinterpret_cast<const float4*>(&pr.d[32 * j + 4 * i]);
-                float w[4] = {s[4 * i] * d.x * exp2f(in_t - in.x),
-                              s[4 * i + 1] * d.y * exp2f(in_t - in.y),
-                              s[4 * i + 2] * d.z * exp2f(in_t - in.z),
-                              s[4 * i + 3] * d.w * exp2f(in_t - in.w)};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (4 * i + e > lane) w[e] = 0.0f;
-                pk[2 * i] = pack_bf16(w[0], w[1]);
-                pk[2 * i + 1] = pack_bf16(w[2], w[3]);
-              }
-            }
-          }
-          // P's columns 16 j .. lie in columns of S that are already read
-          tmem_st16(sbuf + 16 * j, pk);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(BAR_P + (c & 1)));
-          mbar_arrive(bar(BAR_PREPFREE + (c & 1)));
-        }
+        decay = fast_exp2(e);
       }
-      if (c > 0) {
-        const int e = c - 1;
-        if (!wait(BAR_Y, e)) break;
-        tc_fence_after();
-        const long long row = row0 + (long long)e * SB_L + t;
-        const bool live = row < row1;
-        const uint8_t* vrow = sm + SB_V + (e & 1) * SB_PANEL;
-        const float2 f2 = make_float2(f_prev, f_prev);
+      const uint32_t sbuf = tm + TM_S + lanes;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float y1[32], y2[32];
-          tmem_ld32(tm + TM_Y1 + 32 * half + lanes, y1);
-          tmem_ld32(tm + TM_Y2 + 64 * (e & 1) + 32 * half + lanes, y2);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t pk[16];
+        if (j > warp) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = 0u;
+        } else {
+          float s[32];
+          tmem_ld32(sbuf + 32 * j, s);
           tmem_wait_ld();
+          if (j < warp) {
+            const float2 f2 = make_float2(to[j], to[j]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int col = 32 * half + 8 * i;
-            const uint4 vv = *reinterpret_cast<const uint4*>(vrow + tile_offset(t, 4 * half + i));
-            const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
-            float2 o[4];
+            for (int i = 0; i < 8; ++i) {
+              const float4 o = *reinterpret_cast<const float4*>(&pr.out[32 * j + 4 * i]);
+              const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
+                                    make_float2(s[4 * i], s[4 * i + 1]));
+              const float2 v = mul2(mul2(make_float2(o.z, o.w), f2),
+                                    make_float2(s[4 * i + 2], s[4 * i + 3]));
+              pk[2 * i] = pack_bf16(u.x, u.y);
+              pk[2 * i + 1] = pack_bf16(v.x, v.y);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 in = *reinterpret_cast<const float4*>(&pr.in[32 * j + 4 * i]);
+              const float4 d = *reinterpret_cast<const float4*>(&pr.d[32 * j + 4 * i]);
+              float w[4] = {s[4 * i] * d.x * fast_exp2(in_t - in.x),
+                            s[4 * i + 1] * d.y * fast_exp2(in_t - in.y),
+                            s[4 * i + 2] * d.z * fast_exp2(in_t - in.z),
+                            s[4 * i + 3] * d.w * fast_exp2(in_t - in.w)};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (4 * i + e > lane) w[e] = 0.0f;
+              pk[2 * i] = pack_bf16(w[0], w[1]);
+              pk[2 * i + 1] = pack_bf16(w[2], w[3]);
+            }
+          }
+        }
+        // P's columns 16 j .. lie in columns of S that are already read
+        tmem_st16(sbuf + 16 * j, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(BAR_P));
+        mbar_arrive(bar(BAR_PREPFREE + (c & 1)));
+      }
+      const long long first = row0 + (long long)c * SB_L, row = first + t;
+      const bool live = row < row1, whole = first + SB_L <= row1;
+      uint4 zz[8];
+      if (zp) {  // on its way while the products finish
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (live && 8 * i < pn)
+            zz[i] = *reinterpret_cast<const uint4*>(zp + row * a.gate_stride + 8 * i);
+      }
+      if (!wait(BAR_Y2, c) || !wait(BAR_Y, c)) break;
+      tc_fence_after();
+      uint8_t* vtile = sm + SB_V + (c & 1) * SB_PANEL;
+      const float2 f2 = make_float2(decay, decay);
+#pragma unroll
+      for (int part = 0; part < 4; ++part) {
+        float y1[16], y2[16], y3[16];
+        tmem_ld16(tm + TM_Y1 + 16 * part + lanes, y1);
+        tmem_ld16(tm + TM_Y2 + 16 * part + lanes, y2);
+        tmem_ld16(tm + TM_Y2 + 64 + 16 * part + lanes, y3);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ch = 2 * part + i;
+          uint4* place = reinterpret_cast<uint4*>(vtile + tile_offset(t, ch));
+          const uint4 vv = *place;
+          const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
+          float2 o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 8 * i + 2 * j;
+            const float2 r = fma2(f2, make_float2(y3[e], y3[e + 1]),
+                                  fma2(f2, make_float2(y2[e], y2[e + 1]),
+                                       make_float2(y1[e], y1[e + 1])));
+            o[j] = fma2(D2, unpack_bf16(vw[j]), r);
+          }
+          if (zp) {
+            const uint32_t zw[4] = {zz[ch].x, zz[ch].y, zz[ch].z, zz[ch].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 r1 = make_float2(y1[8 * i + 2 * j], y1[8 * i + 2 * j + 1]);
-              const float2 r2 = make_float2(y2[8 * i + 2 * j], y2[8 * i + 2 * j + 1]);
-              o[j] = fma2(D2, unpack_bf16(vw[j]), fma2(f2, r2, r1));
-            }
-            if (live && col < pn) {
-              if (zp) {
-                const uint4 zz =
-                    *reinterpret_cast<const uint4*>(zp + row * a.gate_stride + col);
-                const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float2 z = unpack_bf16(zw[j]);
-                  o[j].x *= gate_act(z.x, a.act);
-                  o[j].y *= gate_act(z.y, a.act);
-                }
-              }
-              uint4 out;
-              out.x = pack_bf16(o[0].x, o[0].y);
-              out.y = pack_bf16(o[1].x, o[1].y);
-              out.z = pack_bf16(o[2].x, o[2].y);
-              out.w = pack_bf16(o[3].x, o[3].y);
-              *reinterpret_cast<uint4*>(yp + (size_t)row * a.H * a.P + col) = out;
+              const float2 z = unpack_bf16(zw[j]);
+              o[j] = mul2(o[j], make_float2(fast_gate_act(z.x, a.act), fast_gate_act(z.y, a.act)));
             }
           }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(BAR_YFREE));
-          mbar_arrive(bar(BAR_VFREE + (e & 1)));
+          const uint4 out = make_uint4(pack_bf16(o[0].x, o[0].y), pack_bf16(o[1].x, o[1].y),
+                                       pack_bf16(o[2].x, o[2].y), pack_bf16(o[3].x, o[3].y));
+          if (whole)
+            *place = out;  // v's last reader leaves y in its place
+          else if (live && 8 * ch < pn)
+            *reinterpret_cast<uint4*>(yp + (size_t)row * a.H * a.P + 8 * ch) = out;
         }
       }
-      f_prev = f_cur;
+      if (whole) fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(BAR_Y2FREE));
+        if (whole) {
+          tma_store_3d(&ba.my, p0, h, (int)first + 32 * warp,
+                       base + SB_V + (c & 1) * SB_PANEL + warp * 4096);
+          tma_store_commit();
+          tma_store_wait_read();
+        }
+        mbar_arrive(bar(BAR_VFREE + (c & 1)));
+      }
     }
   } else if (warp < 8) {
     // ------------------------------------------------ the state: row n = tid - 128
@@ -387,75 +398,30 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     };
     publish();
     bool ok = true;
-    for (int c = 0; c < nb && ok; ++c) {
-      const int stage = c & 1;
-      ok = wait(BAR_PREP + stage, c >> 1) && wait(BAR_VFULL + stage, c >> 1) &&
-           wait(BAR_KFULL + stage, c >> 1);
+    for (int c = 0; c < nb; ++c) {
+      ok = wait(BAR_PREP + (c & 1), c >> 1);
       if (!ok) break;
       const SsmPrep& pr = *prep(c);
-      uint8_t* vtile = sm + SB_V + stage * SB_PANEL;
-      const long long left = row1 - (row0 + (long long)c * SB_L);
-      const int live = left < SB_L ? (int)left : SB_L;
-      for (int qd = 0; qd < 4 && ok; ++qd) {
-        const int use = 4 * c + qd, buf = use & 1;
-        const int rq = n >> 2, t = 32 * qd + rq;
-        const float w = pr.w[t];
-        if (use >= 2) ok = wait(BAR_WFREE + buf, (use >> 1) - 1);
-        if (!ok) break;
-        uint8_t* wt = sm + SB_W + buf * 3 * SB_WPART;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int ch = 2 * (n & 3) + i;
-          const uint32_t vo = tile_offset(t, ch), wo = tile_offset(rq, ch);
-          uint32_t p1[4] = {0, 0, 0, 0}, p2[4] = {0, 0, 0, 0}, p3[4] = {0, 0, 0, 0};
-          if (t < live) {
-            const uint4 vv = *reinterpret_cast<const uint4*>(vtile + vo);
-            const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float2 x = unpack_bf16(vw[j]);
-              x.x *= w;
-              x.y *= w;
-              p1[j] = pack_bf16(x.x, x.y);
-              float2 r = unpack_bf16(p1[j]);
-              x.x -= r.x;
-              x.y -= r.y;
-              p2[j] = pack_bf16(x.x, x.y);
-              r = unpack_bf16(p2[j]);
-              p3[j] = pack_bf16(x.x - r.x, x.y - r.y);
-            }
-          } else {
-            // rows behind the segment's end, whatever they hold, become zeros
-            *reinterpret_cast<uint4*>(vtile + vo) = make_uint4(0, 0, 0, 0);
-            for (int pl = 0; pl < npanels; ++pl)
-              *reinterpret_cast<uint4*>(sm + SB_K + (2 * stage + pl) * SB_PANEL + vo) =
-                  make_uint4(0, 0, 0, 0);
-          }
-          *reinterpret_cast<uint4*>(wt + wo) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-          *reinterpret_cast<uint4*>(wt + SB_WPART + wo) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-          *reinterpret_cast<uint4*>(wt + 2 * SB_WPART + wo) =
-              make_uint4(p3[0], p3[1], p3[2], p3[3]);
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_WREADY + buf));
-      }
-      if (!ok) break;
       const float keep = exp2f((pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]));
-      if (lane == 0) mbar_arrive(bar(BAR_CLEAN + stage));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 1)));
       ok = wait(BAR_DM, c);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float r[32];
-        tmem_ld32(tm + TM_DM + 32 * half + lanes, r);
+      for (int part = 0; part < 4; ++part) {
+        float r1[16], r2[16], r3[16];
+        tmem_ld16(tm + TM_DM + 16 * part + lanes, r1);
+        tmem_ld16(tm + TM_DM + 64 + 16 * part + lanes, r2);
+        tmem_ld16(tm + TM_DM + 128 + 16 * part + lanes, r3);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) st[32 * half + i] = fmaf(st[32 * half + i], keep, r[i]);
+        for (int i = 0; i < 16; ++i)
+          st[16 * part + i] = fmaf(st[16 * part + i], keep, r1[i] + (r2[i] + r3[i]));
       }
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + stage));
+      if (lane == 0) mbar_arrive(bar(BAR_DMFREE));
       if (c + 1 < nb) {
         ok = wait(BAR_HFREE, c);
         if (!ok) break;
@@ -469,106 +435,204 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           *reinterpret_cast<float4*>(mrow + i) =
               make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
     }
-  } else if (warp == 8) {
-    if (lane == 0) {
-      constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY2 = mma_desc(128, 64, 0, 1),
-                         dY1 = mma_desc(128, 64, 0, 1);
-      for (int c = 0; c <= nb; ++c) {
-        if (c < nb) {
-          const int stage = c & 1;
-          const uint32_t q = base + SB_Q + stage * 2 * SB_PANEL,
-                         k = base + SB_K + stage * 2 * SB_PANEL;
-          if (!wait(BAR_QFULL + stage, c >> 1) || !wait(BAR_KFULL + stage, c >> 1)) break;
-          tc_fence_after();
-          for (int i = 0; i < nk; ++i) {
-            const uint32_t o = (i >> 2) * SB_PANEL + (i & 3) * 32;
-            mma_ss(tm + TM_S + stage * 128, tile_desc(q + o), tile_desc(k + o), dS, i > 0);
-          }
-          mma_commit(bar(BAR_S + stage));
-          mma_commit(bar(BAR_KFREE + stage));
-          // Y1 and this block's half of Y2 were last read two blocks ago
-          if ((c >= 2 && !wait(BAR_YFREE, c - 2)) || !wait(BAR_HREADY, c)) break;
-          tc_fence_after();
-          for (int part = 0; part < 2; ++part)
-            for (int i = 0; i < nk; ++i) {
-              const uint32_t o = (i >> 2) * SB_PANEL + (i & 3) * 32;
-              mma_ss(tm + TM_Y2 + stage * 64, tile_desc(q + o),
-                     tile_desc(base + SB_H + part * SB_PANEL + i * 2048), dY2, part + i > 0);
-            }
-          mma_commit(bar(BAR_QFREE + stage));
-          mma_commit(bar(BAR_HFREE));
+  } else if (warp < 12) {
+    // ------------------------------------------------ w o v in three bf16 parts
+    const int i0 = tid - 256, rq = i0 >> 2;  // row in the quarter, and 16 of its values
+    for (int c = 0; c < nb; ++c) {
+      const int stage = c & 1;
+      if (!wait(BAR_PREP + stage, c >> 1) || !wait(BAR_VFULL + stage, c >> 1)) break;
+      uint8_t* vtile = sm + SB_V + stage * SB_PANEL;
+      const long long left = row1 - (row0 + (long long)c * SB_L);
+      uint4 vv[8];
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        vv[i] = *reinterpret_cast<const uint4*>(
+            vtile + tile_offset(32 * (i >> 1) + rq, 2 * (i0 & 3) + (i & 1)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = prep(c)->w[32 * i + rq];
+      if (left < SB_L) {
+        // rows behind the segment's end, whatever they hold, become zeros
+        if (!wait(BAR_KFULL + stage, c >> 1)) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = 32 * (i >> 1) + rq;
+          if (t < left) continue;
+          const uint32_t o = tile_offset(t, 2 * (i0 & 3) + (i & 1));
+          vv[i] = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vtile + o) = vv[i];
+          for (int pl = 0; pl < npanels; ++pl)
+            *reinterpret_cast<uint4*>(sm + SB_K + (2 * stage + pl) * SB_PANEL + o) = vv[i];
         }
-        if (c > 0) {
-          const int e = c - 1;
-          if (!wait(BAR_P + (e & 1), e >> 1) || !wait(BAR_VFULL + (e & 1), e >> 1) ||
-              !wait(BAR_CLEAN + (e & 1), e >> 1) || (c == nb && c >= 2 && !wait(BAR_YFREE, c - 2)))
-            break;
-          tc_fence_after();
+      }
+      bool ok = true;
+#pragma unroll
+      for (int qd = 0; qd < 4; ++qd) {
+        const int use = 4 * c + qd, buf = qd & 1;
+        uint32_t p[3][8];
+        const float2 w2 = make_float2(w[qd], w[qd]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 u = vv[2 * qd + (j >> 2)];
+          const uint32_t word = (j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w;
+          float2 x = mul2(unpack_bf16(word), w2);
+          p[0][j] = pack_bf16(x.x, x.y);
+          x = sub2(x, unpack_bf16(p[0][j]));
+          p[1][j] = pack_bf16(x.x, x.y);
+          x = sub2(x, unpack_bf16(p[1][j]));
+          p[2][j] = pack_bf16(x.x, x.y);
+        }
+        ok = ok && (use < 2 || wait(BAR_WFREE + buf, (use >> 1) - 1));
+        uint8_t* wt = sm + SB_W + buf * 3 * SB_WPART;
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint4*>(wt + part * SB_WPART + tile_offset(rq, 2 * (i0 & 3) + i)) =
+                make_uint4(p[part][4 * i], p[part][4 * i + 1], p[part][4 * i + 2],
+                           p[part][4 * i + 3]);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_WREADY + buf));
+      }
+      if (lane == 0) {
+        mbar_arrive(bar(BAR_CLEAN + stage));
+        mbar_arrive(bar(BAR_PREPFREE + stage));
+      }
+      if (!ok) break;
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------ products S and Y1
+    constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY1 = mma_desc(128, 64, 0, 1);
+    const uint32_t q0 = tile_desc(base + SB_Q), k0 = tile_desc(base + SB_K),
+                   v0 = tile_desc(base + SB_V);
+    for (int c = 0; c <= nb; ++c) {
+      if (c > 0) {
+        const int e = c - 1;
+        const uint32_t stage = e & 1;
+        if (!wait(BAR_CLEAN + stage, e >> 1) || !wait(BAR_VFULL + stage, e >> 1) ||
+            !wait(BAR_P, e))
+          break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t v = v0 + stage * (SB_PANEL >> 4);
+#pragma unroll
           for (int i = 0; i < SB_L / 16; ++i)
-            mma_ts(tm + TM_Y1, tm + TM_S + (e & 1) * 128 + 8 * i,
-                   tile_desc(base + SB_V + (e & 1) * SB_PANEL + i * 2048), dY1, i > 0);
+            mma_ts(tm + TM_Y1, tm + TM_S + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
           mma_commit(bar(BAR_Y));
         }
+        __syncwarp();
       }
-      mma_commit(bar(BAR_DRAIN));
-      mbar_wait(bar(BAR_DRAIN), 0, abort);
-    }
-  } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr uint32_t dM = mma_desc(128, 64, 1, 1);
-      bool ok = true;
-      for (int c = 0; c < nb && ok; ++c) {
-        const int stage = c & 1;
-        const uint32_t k = base + SB_K + stage * 2 * SB_PANEL;
-        ok = wait(BAR_KFULL + stage, c >> 1);
-        for (int qd = 0; qd < 4 && ok; ++qd) {
-          const int use = 4 * c + qd, buf = use & 1;
-          ok = wait(BAR_WREADY + buf, use >> 1);
-          if (!ok) break;
-          tc_fence_after();
-          for (int part = 0; part < 3; ++part)
-            for (int i = 0; i < 2; ++i)
-              mma_ss(tm + TM_DM, tile_desc(k + qd * 4096 + i * 2048, SB_PANEL),
-                     tile_desc(base + SB_W + (buf * 3 + part) * SB_WPART + i * 2048), dM,
-                     qd + part + i > 0);
-          mma_commit(bar(BAR_WFREE + buf));
+      if (c < nb) {
+        const uint32_t stage = c & 1;
+        if (!wait(BAR_QFULL + stage, c >> 1) || !wait(BAR_KFULL + stage, c >> 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t q = q0 + stage * (2 * SB_PANEL >> 4), k = k0 + stage * (2 * SB_PANEL >> 4);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t o = ((i >> 2) * SB_PANEL + (i & 3) * 32) >> 4;
+            if (i < nk) mma_ss(tm + TM_S, q + o, k + o, dS, i > 0);
+          }
+          mma_commit(bar(BAR_S));
+          mma_commit(bar(BAR_KFREE + stage));
+          mma_commit(bar(BAR_QFREE + stage));
         }
-        if (!ok) break;
-        mma_commit(bar(BAR_DM));
-        mma_commit(bar(BAR_KFREE + stage));
+        __syncwarp();
       }
-      mma_commit(bar(BAR_DRAIN + 1));
-      mbar_wait(bar(BAR_DRAIN + 1), 0, abort);
     }
-  } else if (warp == 10) {
+    if (elect_one()) mma_commit(bar(BAR_DRAIN));
+    __syncwarp();
+    mbar_wait(bar(BAR_DRAIN), 0, abort);
+  } else if (warp == 13) {
+    // ------------------------------------------------ product dM
+    constexpr uint32_t dM = mma_desc(128, 192, 1, 1);
+    const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W, SB_WPART);
+    bool ok = true;
+    for (int c = 0; c < nb && ok; ++c) {
+      const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
+      ok = wait(BAR_KFULL + stage, c >> 1) && (c == 0 || wait(BAR_DMFREE, c - 1));
+      for (int qd = 0; qd < 4 && ok; ++qd) {
+        const uint32_t use = 4 * c + qd, buf = use & 1;
+        ok = wait(BAR_WREADY + buf, use >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t kq = k + qd * (4096 >> 4), w = w0 + buf * (3 * SB_WPART >> 4);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            mma_ss(tm + TM_DM, kq + i * (2048 >> 4), w + i * (2048 >> 4), dM, qd + i > 0);
+          mma_commit(bar(BAR_WFREE + buf));
+          if (qd == 3) {
+            mma_commit(bar(BAR_DM));
+            mma_commit(bar(BAR_KFREE + stage));
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) mma_commit(bar(BAR_DRAIN + 1));
+    __syncwarp();
+    mbar_wait(bar(BAR_DRAIN + 1), 0, abort);
+  } else if (warp == 14) {
+    // ------------------------------------------------ loads: each tile as soon as its place is free
     if (lane == 0) {
-      int issued = 0;
-      for (int c = 0; c < nb; ++c) {
-        const int stage = c & 1, r = (int)(row0 + (long long)c * SB_L);
-        if (c >= 2 && !wait(BAR_KFREE + stage, (c >> 1) - 1)) break;
-        mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
-        for (int pl = 0; pl < npanels; ++pl)
-          tma_load_3d(base + SB_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
-                      bar(BAR_KFULL + stage));
-        if (c >= 2 && !wait(BAR_VFREE + stage, (c >> 1) - 1)) { issued = 3 * c + 1; break; }
-        mbar_expect(bar(BAR_VFULL + stage), SB_PANEL);
-        tma_load_3d(base + SB_V + stage * SB_PANEL, &ba.mv, p0, h, r, bar(BAR_VFULL + stage));
-        if (c >= 2 && !wait(BAR_QFREE + stage, (c >> 1) - 1)) { issued = 3 * c + 2; break; }
-        mbar_expect(bar(BAR_QFULL + stage), npanels * SB_PANEL);
-        for (int pl = 0; pl < npanels; ++pl)
-          tma_load_3d(base + SB_Q + (2 * stage + pl) * SB_PANEL, &ba.mq, 64 * pl, g, r,
-                      bar(BAR_QFULL + stage));
-        issued = 3 * c + 3;
+      int kc = 0, vc = 0, qc = 0;  // blocks whose load is issued
+      const int r0 = (int)row0;
+      unsigned long long since = 0;
+      while (kc < nb || vc < nb || qc < nb) {
+        bool moved = false;
+        auto may = [&](int c, int free_bar) {
+          return c < nb &&
+                 (c < 2 || mbar_test(bar(free_bar + (c & 1)), (uint32_t)((c >> 1) - 1) & 1u));
+        };
+        if (may(qc, BAR_QFREE)) {
+          const uint32_t stage = qc & 1;
+          mbar_expect(bar(BAR_QFULL + stage), npanels * SB_PANEL);
+          for (int pl = 0; pl < npanels; ++pl)
+            tma_load_3d(base + SB_Q + (2 * stage + pl) * SB_PANEL, &ba.mq, 64 * pl, g,
+                        r0 + qc * SB_L, bar(BAR_QFULL + stage));
+          ++qc;
+          moved = true;
+        }
+        if (may(kc, BAR_KFREE)) {
+          const uint32_t stage = kc & 1;
+          mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
+          for (int pl = 0; pl < npanels; ++pl)
+            tma_load_3d(base + SB_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g,
+                        r0 + kc * SB_L, bar(BAR_KFULL + stage));
+          ++kc;
+          moved = true;
+        }
+        if (may(vc, BAR_VFREE)) {
+          const uint32_t stage = vc & 1;
+          mbar_expect(bar(BAR_VFULL + stage), SB_PANEL);
+          tma_load_3d(base + SB_V + stage * SB_PANEL, &ba.mv, p0, h, r0 + vc * SB_L,
+                      bar(BAR_VFULL + stage));
+          ++vc;
+          moved = true;
+        }
+        if (moved) {
+          since = 0;
+          continue;
+        }
+        if (*abort) break;
+        const unsigned long long now = wall_ns();
+        if (since == 0) since = now;
+        if (now - since > MBAR_LIMIT_NS) {
+          *abort = 1;
+          record_status(STATUS_TIMEOUT);
+          break;
+        }
+        __nanosleep(40);
       }
       if (*abort) {
         // loads in flight land before the block's memory is given up (each wait limited)
         int none = 0;
-        const int kc = (issued + 2) / 3, vc = (issued + 1) / 3, qc = issued / 3;
-        for (int back = 1; back <= 2; ++back) {
-          if (kc >= back) mbar_wait(bar(BAR_KFULL + ((kc - back) & 1)), ((kc - back) >> 1) & 1, &none);
-          if (vc >= back) mbar_wait(bar(BAR_VFULL + ((vc - back) & 1)), ((vc - back) >> 1) & 1, &none);
-          if (qc >= back) mbar_wait(bar(BAR_QFULL + ((qc - back) & 1)), ((qc - back) >> 1) & 1, &none);
-        }
+        const int n[3] = {qc, kc, vc}, full[3] = {BAR_QFULL, BAR_KFULL, BAR_VFULL};
+        for (int i = 0; i < 3; ++i)
+          for (int c = n[i] > 2 ? n[i] - 2 : 0; c < n[i]; ++c)
+            mbar_wait(bar(full[i] + (c & 1)), (uint32_t)(c >> 1) & 1u, &none);
       }
     }
   } else {
@@ -584,7 +648,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
     };
     fetch(0);
-    for (int c = 0; c < nb; ++c) {
+    auto prepare = [&](int c) -> bool {
       float d[4], la[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -628,7 +692,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         out[i] = d[i] * exp2f(tail[i]);
         w[i] = d[i] * exp2f(tail[i] + later);
       }
-      if (c >= 2 && !wait(BAR_PREPFREE + (c & 1), (c >> 1) - 1)) break;
+      if (c >= 2 && !wait(BAR_PREPFREE + (c & 1), (c >> 1) - 1)) return false;
       SsmPrep* pr = prep(c);
       reinterpret_cast<float4*>(pr->d)[lane] = make_float4(d[0], d[1], d[2], d[3]);
       reinterpret_cast<float4*>(pr->in)[lane] = make_float4(in[0], in[1], in[2], in[3]);
@@ -637,7 +701,34 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       if (lane < 4) pr->run[lane] = lane == 0 ? run[0] : lane == 1 ? run[1] : lane == 2 ? run[2] : run[3];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_PREP + (c & 1)));
+      return true;
+    };
+    constexpr uint32_t dY2 = mma_desc(128, 128, 0, 1);
+    const uint32_t q0 = tile_desc(base + SB_Q), h0 = tile_desc(base + SB_H, SB_PANEL);
+    bool ok = prepare(0) && (nb < 2 || prepare(1));
+    for (int c = 0; c < nb && ok; ++c) {
+      const uint32_t stage = c & 1;
+      ok = wait(BAR_HREADY, c) && wait(BAR_QFULL + stage, c >> 1) &&
+           (c == 0 || wait(BAR_Y2FREE, c - 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t q = q0 + stage * (2 * SB_PANEL >> 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t o = ((i >> 2) * SB_PANEL + (i & 3) * 32) >> 4;
+          if (i < nk) mma_ss(tm + TM_Y2, q + o, h0 + i * (2048 >> 4), dY2, i > 0);
+        }
+        mma_commit(bar(BAR_Y2));
+        mma_commit(bar(BAR_HFREE));
+        mma_commit(bar(BAR_QFREE + stage));
+      }
+      __syncwarp();
+      if (c + 2 < nb) ok = prepare(c + 2);
     }
+    if (elect_one()) mma_commit(bar(BAR_DRAIN + 2));
+    __syncwarp();
+    mbar_wait(bar(BAR_DRAIN + 2), 0, abort);
   }
   tc_fence_before();
   __syncthreads();
