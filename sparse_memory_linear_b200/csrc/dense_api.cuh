@@ -196,15 +196,15 @@ EncodeTiledFn tensor_map_encoder() {
   return fn;
 }
 
-// Rows of `heads` x `width` bf16 values at a pitch, moved in tiles of `box_rows` rows x 64 values
-// of one head; loads give zeros where the head or the rows end, stores stop there.
+// Rows of `heads` x `width` bf16 values at a pitch, read in tiles of 128 rows x 64 values of one
+// head, with zeros where the head or the rows end.
 bool tile_map(CUtensorMap* map, const void* p, int width, int heads, long long rows,
-              long long pitch, int box_rows) {
+              long long pitch) {
   const EncodeTiledFn encode = tensor_map_encoder();
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)pitch * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, steps[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, SB_L}, steps[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box,
                 steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -217,21 +217,72 @@ bool ssm_block_fits(const sdm_ssm_shape& s, long long R) {
   return s.in_dtype == SDM_BF16 && s.N <= 128 && s.T >= 16 && R < 2147483647LL;
 }
 
-sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, cudaStream_t st) {
-  DeviceInfo* di;
-  const sdm_status rc = device_info(&di);
-  if (rc != SDM_OK) return rc;
+// How the block-wise scan cuts sequences into segments.  A CTA walks one segment of one (head, 64
+// columns) tile at one block of 128 tokens in about SSM_WALK_US; a pass that makes the segments'
+// own contributions costs SSM_PRE_US a block, and with the chain over segments SSM_SPLIT_US at
+// least.  The number of segments is the one with the least estimated time; packed batches,
+// whose lengths only the device knows, are cut as one sequence of all rows would be.
+constexpr double SSM_WALK_US = 3.0, SSM_PRE_US = 0.7, SSM_SPLIT_US = 12.0;
+
+struct SsmPlan {
+  long long seg_blocks, items;  // blocks of a segment; (sequence, segment) pairs at most
+  bool split;
+  size_t off_decays, bytes;
+};
+
+SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms) {
+  const long long L = ((long long)s.T + SB_L - 1) / SB_L, units = (long long)s.H *
+                  ((s.d_v + SB_P - 1) / SB_P), seqs = packed ? 1 : s.B;
+  auto waves = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
+  long long best = 1;
+  double least = waves(seqs * units) * L * SSM_WALK_US;
+  const long long most = 6LL * sms / (seqs * units) + 1;  // more waves gain nothing
+  for (long long n = 2; n <= L && n <= most; ++n) {
+    const long long len = (L + n - 1) / n, segs = (L + len - 1) / len;
+    if (segs != n) continue;
+    const double t = waves(seqs * n * units) * len * SSM_WALK_US +
+                     waves(seqs * (n - 1) * units) * len * SSM_PRE_US + SSM_SPLIT_US;
+    if (t < least) {
+      least = t;
+      best = n;
+    }
+  }
+  SsmPlan p = {};
+  p.split = best > 1;
+  p.seg_blocks = L > 0 ? (L + best - 1) / best : 1;
+  const long long seg_rows = p.seg_blocks * SB_L;
+  p.items = packed ? s.T / seg_rows + s.B : s.B * (s.T > 0 ? (s.T + seg_rows - 1) / seg_rows : 1);
+  if (p.split) {
+    p.off_decays = round_up((size_t)p.items * s.H * s.N * s.d_v * 4, WS_ALIGN);
+    p.bytes = p.off_decays + round_up((size_t)p.items * s.H * 4, WS_ALIGN);
+  }
+  return p;
+}
+
+sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceInfo* di, void* ws,
+                         cudaStream_t st) {
+  const SsmPlan plan = ssm_plan(s, a.seq.cu != nullptr, di->sms);
   SsmBlockArgs ba;
   ba.a = a;
-  ba.seg_blocks = 1 << 24;
+  ba.seg_blocks = (int)plan.seg_blocks;
   ba.ptiles = (s.d_v + SB_P - 1) / SB_P;
-  if (!tile_map(&ba.mq, a.q, s.N, s.G, a.seq.R, a.q_stride, SB_L) ||
-      !tile_map(&ba.mk, a.k, s.N, s.G, a.seq.R, a.k_stride, SB_L) ||
-      !tile_map(&ba.mv, a.v, s.d_v, s.H, a.seq.R, a.v_stride, SB_L) ||
-      !tile_map(&ba.my, a.y, s.d_v, s.H, a.seq.R, (long long)s.H * s.d_v, 32))
+  ba.starts = static_cast<float*>(ws);
+  ba.decays = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.off_decays);
+  if (!tile_map(&ba.mq, a.q, s.N, s.G, a.seq.R, a.q_stride) ||
+      !tile_map(&ba.mk, a.k, s.N, s.G, a.seq.R, a.k_stride) ||
+      !tile_map(&ba.mv, a.v, s.d_v, s.H, a.seq.R, a.v_stride))
     return SDM_ERR_CUDA;
-  const long long items = s.B, blocks = items * s.H * ba.ptiles;
+  const long long blocks = plan.items * s.H * ba.ptiles;
   if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;
+  if (plan.split) {
+    SDM_CUDA_TRY(launch_pdl(ssm_segment_kernel, dim3((unsigned)blocks), dim3(SG_THREADS),
+                            (size_t)SG_SMEM, st, ba));
+    SDM_CUDA_TRY(launch_pdl(ssm_chain_kernel,
+                            dim3((unsigned)s.B, (unsigned)s.H,
+                                 (unsigned)((s.N * s.d_v / 4 + 255) / 256)),
+                            dim3(256), 0, st, ba));
+    g_launches.fetch_add(2, std::memory_order_relaxed);
+  }
   SDM_CUDA_TRY(launch_pdl(ssm_block_kernel, dim3((unsigned)blocks), dim3(SB_THREADS),
                           (size_t)SB_SMEM, st, ba));
   g_launches.fetch_add(1, std::memory_order_relaxed);
@@ -276,8 +327,17 @@ sdm_status sdm_conv_step(const void* x, const float* w, const float* bias, void*
 
 size_t sdm_ssm_workspace_size(sdm_ssm_shape shape) {
   SsmArgs a;
+  DeviceInfo* di;
   if (!ssm_args(shape, false, &a)) return 0;
-  return WS_ALIGN;
+  size_t need = WS_ALIGN;
+  if (!ssm_block_fits(shape, 0)) return need;
+  // without a device (sizes asked for ahead of time) a B200's number of multiprocessors
+  const int sms = device_info(&di) == SDM_OK ? di->sms : 148;
+  for (const bool packed : {false, true}) {
+    const size_t n = ssm_plan(shape, packed, sms).bytes;
+    if (n > need) need = n;
+  }
+  return need;
 }
 
 sdm_status sdm_ssm_forward(const void* k, const void* q, const void* v, const void* dt,
@@ -302,10 +362,13 @@ sdm_status sdm_ssm_forward(const void* k, const void* q, const void* v, const vo
       SDM_CUDA_TRY(cudaMemsetAsync(M, 0, (size_t)s.B * s.H * s.N * s.d_v * 4, st));
     return SDM_OK;
   }
+  DeviceInfo* di;
+  const sdm_status rc = device_info(&di);
+  if (rc != SDM_OK) return rc;
   a.seq = SeqBounds{cu, s.B, s.T, R};
   a.from_zero = init == SDM_INIT_ZERO;
   ProfScope ps(SDM_KERNEL_SSM, st);
-  if (ssm_block_fits(s, R)) return ssm_block_run(s, a, st);
+  if (ssm_block_fits(s, R)) return ssm_block_run(s, a, di, ws, st);
   const dim3 grid((unsigned)s.B, (unsigned)s.H, (unsigned)((s.d_v + SSM_COLS - 1) / SSM_COLS));
   if (s.in_dtype == SDM_BF16)
     SDM_CUDA_TRY(launch_ssm_scan<__nv_bfloat16>(a, grid, st));

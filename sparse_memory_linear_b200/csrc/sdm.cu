@@ -150,6 +150,9 @@ sdm_status device_info(DeviceInfo** out) {
     SDM_CUDA_TRY(cudaFuncSetAttribute(ssm_block_kernel,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       (int)SB_SMEM));
+    SDM_CUDA_TRY(cudaFuncSetAttribute(ssm_segment_kernel,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)SG_SMEM));
     d.attrs_set = true;
   }
   *out = &d;

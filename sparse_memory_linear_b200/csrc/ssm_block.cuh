@@ -8,7 +8,8 @@
 //   S  = q k^T                      128 x 128 x N
 //   Y2 = q M                        128 x (2 x 64) x N, M as two bf16 parts (16 bits of it)
 //   Y1 = (S o weights) v            128 x 64 x 128, weights rounded to bf16
-//   dM = k^T (w o v)                N x (3 x 64) x 128, w o v as three bf16 parts (24 bits)
+//   dM = k^T (w o v)                N x (2 x 64) x 128 and N x 64 x 128, w o v as three bf16
+//                                   parts (24 bits)
 // The parts lie side by side as columns of one product, so that q and k are read from shared
 // memory once for all of them: its bandwidth is what the matrix unit waits for at these sizes.
 // The state is kept in fp32 registers and never rounded to less: dM has to be exact to fp32,
@@ -16,15 +17,16 @@
 // weight in another's read (half a step of bf16); two parts of M keep the second term below
 // that.
 //
-// One CTA walks the blocks of (sequence segment, head, 64 value columns) in order:
-//   warps 0-3    a thread per token row: weighs S into P (tensor memory), then joins
-//                y = exp(c_t) Y2 + Y1 + D v, gates and stores it
-//   warps 4-7    a thread per state row: adds dM to the decayed state, publishes its two parts
-//   warps 8-11   a thread per quarter row of v: w o v in parts
-//   warp 12      issues S, Y1            warp 13  issues dM
-//   warp 14      TMA loads of q, k, v    warp 15  step sizes and decay sums, two blocks ahead;
-//                                                 issues Y2
-// joined by mbarriers.
+// One CTA walks the blocks of (sequence segment, head, 64 value columns) in order, five groups of
+// four warps each at its own block:
+//   P   a thread per token row: weighs S into P (tensor memory, in place)
+//   Y   a thread per token row: y = exp(c_t) Y2 + Y1 + D v, gated and stored
+//   H   a thread per state row: adds dM to the decayed state, publishes the state's two parts
+//   W   a thread per quarter row of v: w o v in parts, 32 tokens at a time
+//   and four single warps: S and Y1; dM; TMA loads of q, k, v; step sizes and decay sums two
+//   blocks ahead, with Y2
+// joined by mbarriers.  A block's work is a chain of short dependent steps; with the steps on
+// warps of their own the chains of successive blocks overlap.
 //
 // Decays are summed within runs of 32 tokens (a warp's rows) and the runs' totals added, never as
 // differences of long sums: exp(c_t - c_s) is one exponential inside a run, and the product of
@@ -39,7 +41,7 @@ namespace sdm {
 
 constexpr int SB_L = 128;      // tokens of a block
 constexpr int SB_P = 64;       // value columns of a CTA
-constexpr int SB_THREADS = 512;
+constexpr int SB_THREADS = 640;
 
 // Shared memory, from a 1024-byte boundary.
 constexpr uint32_t SB_PANEL = 16384;                       // 128 rows of 128 bytes
@@ -62,24 +64,27 @@ constexpr uint32_t SB_BARS = SB_PREP + 2 * sizeof(SsmPrep);
 enum {
   BAR_QFULL = 0, BAR_QFREE = 2, BAR_KFULL = 4, BAR_KFREE = 6, BAR_VFULL = 8, BAR_VFREE = 10,
   BAR_PREP = 12, BAR_PREPFREE = 14, BAR_WREADY = 16, BAR_WFREE = 18, BAR_CLEAN = 20,
-  BAR_S = 22, BAR_P, BAR_Y, BAR_Y2, BAR_Y2FREE, BAR_DM, BAR_DMFREE, BAR_HREADY, BAR_HFREE,
-  BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 3
+  BAR_S = 22, BAR_P = 24, BAR_Y = 26, BAR_YFREE = 28, BAR_Y2, BAR_Y2FREE, BAR_DM, BAR_DMFREE,
+  BAR_HREADY, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 3
 };
 constexpr uint32_t SB_TMEM_PTR = SB_BARS + 40 * 8;
 static_assert(BAR_COUNT <= 40, "barriers");
 constexpr uint32_t SB_SMEM = SB_TMEM_PTR + 32 + 1024;      // and room to align
 static_assert(SB_SMEM <= 232448 - 64, "shared memory of a block");
 
-// Tensor memory columns; P takes the first half of S's.
-constexpr uint32_t TM_S = 0, TM_Y1 = 128, TM_Y2 = 192, TM_DM = 320;
+// Tensor memory columns: two buffers of S, whose first half becomes P and whose second half,
+// once weighed, holds Y1; Y2 and dM of one block.
+constexpr uint32_t TM_S = 0, TM_Y1 = 64, TM_Y2 = 256, TM_DM = 384;
 
 constexpr float SB_LOG2E = 1.4426950408889634f;
 
 struct SsmBlockArgs {
   SsmArgs a;
-  CUtensorMap mq, mk, mv, my;
+  CUtensorMap mq, mk, mv;
   int seg_blocks;   // blocks of a segment
   int ptiles;       // 64-column tiles of d_v
+  float* starts;    // [items, H, N, P]: the state before each segment of a split sequence
+  float* decays;    // [items, H]: the segment's whole decay
 };
 
 // The (sequence, segment) of work item `item`: a sequence of n rows has max(1, ceil(n / seg))
@@ -116,6 +121,77 @@ __device__ __forceinline__ bool ssm_find_item(const SeqBounds& seq, long long it
     item -= __shfl_sync(FULL_MASK, upto, 31);
   }
   return false;
+}
+
+// A block's step sizes and decay sums, by one warp: lane l holds tokens 4 l .. 4 l + 3.
+struct SsmSums {
+  float d[4], in[4], tail[4];  // step size; log2 decays from the run's start, to the run's end
+  float run[4], later;         // log2 decay of each run, and of the runs behind this lane's
+};
+__device__ __forceinline__ void ssm_sums(const float raw[4], const bool live[4], float bias,
+                                         float A2, int softplus, SsmSums& o) {
+  const int lane = threadIdx.x & 31;
+  float la[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o.d[i] = live[i] ? ssm_step_size(raw[i] + bias, softplus) : 0.0f;
+    // 2^-160 is 0 in fp32: a stronger decay changes nothing and would cost the sums their low
+    // bits
+    la[i] = fmaxf(o.d[i] * A2, -160.0f);
+  }
+  const float own = (la[0] + la[1]) + (la[2] + la[3]);
+  float up = own, down = own;  // sums over the run's 8 lanes, from its start and from its end
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) {
+    const float p = __shfl_up_sync(FULL_MASK, up, s, 8);
+    const float n = __shfl_down_sync(FULL_MASK, down, s, 8);
+    if ((lane & 7) >= s) up += p;
+    if ((lane & 7) + s < 8) down += n;
+  }
+  float before = __shfl_up_sync(FULL_MASK, up, 1, 8),
+        after = __shfl_down_sync(FULL_MASK, down, 1, 8);
+  if ((lane & 7) == 0) before = 0.0f;
+  if ((lane & 7) == 7) after = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o.run[j] = __shfl_sync(FULL_MASK, up, 8 * j + 7);
+  o.later = 0.0f;
+#pragma unroll
+  for (int j = 3; j >= 1; --j)
+    if (j > (lane >> 3)) o.later += o.run[j];
+  o.in[0] = before + la[0];
+  o.in[1] = before + (la[0] + la[1]);
+  o.in[2] = before + (la[0] + la[1] + la[2]);
+  o.in[3] = before + own;
+  o.tail[0] = after + (la[1] + la[2] + la[3]);
+  o.tail[1] = after + (la[2] + la[3]);
+  o.tail[2] = after + la[3];
+  o.tail[3] = after;
+}
+
+// Eight pairs of values times w, in three bf16 parts.
+__device__ __forceinline__ void ssm_parts(const uint4& va, const uint4& vb, float w,
+                                          uint32_t p[3][8]) {
+  const float2 w2 = make_float2(w, w);
+  const uint32_t vw[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float2 x = mul2(unpack_bf16(vw[j]), w2);
+    p[0][j] = pack_bf16(x.x, x.y);
+    x = sub2(x, unpack_bf16(p[0][j]));
+    p[1][j] = pack_bf16(x.x, x.y);
+    x = sub2(x, unpack_bf16(p[1][j]));
+    p[2][j] = pack_bf16(x.x, x.y);
+  }
+}
+__device__ __forceinline__ void ssm_store_parts(uint8_t* place, uint32_t o0, uint32_t o1,
+                                                const uint32_t p[3][8]) {
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    *reinterpret_cast<uint4*>(place + part * SB_WPART + o0) =
+        make_uint4(p[part][0], p[part][1], p[part][2], p[part][3]);
+    *reinterpret_cast<uint4*>(place + part * SB_WPART + o1) =
+        make_uint4(p[part][4], p[part][5], p[part][6], p[part][7]);
+  }
 }
 
 __global__ void __launch_bounds__(SB_THREADS, 1)
@@ -174,16 +250,17 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       mbar_init(bar(BAR_KFULL + i), 1);
       mbar_init(bar(BAR_KFREE + i), 2);
       mbar_init(bar(BAR_VFULL + i), 1);
-      mbar_init(bar(BAR_VFREE + i), 4);
+      mbar_init(bar(BAR_VFREE + i), 5);
       mbar_init(bar(BAR_PREP + i), 1);
-      mbar_init(bar(BAR_PREPFREE + i), 12);
+      mbar_init(bar(BAR_PREPFREE + i), 16);
       mbar_init(bar(BAR_WREADY + i), 4);
       mbar_init(bar(BAR_WFREE + i), 1);
       mbar_init(bar(BAR_CLEAN + i), 4);
+      mbar_init(bar(BAR_S + i), 1);
+      mbar_init(bar(BAR_P + i), 4);
+      mbar_init(bar(BAR_Y + i), 1);
     }
-    mbar_init(bar(BAR_S), 1);
-    mbar_init(bar(BAR_P), 4);
-    mbar_init(bar(BAR_Y), 1);
+    mbar_init(bar(BAR_YFREE), 4);
     mbar_init(bar(BAR_Y2), 1);
     mbar_init(bar(BAR_Y2FREE), 4);
     mbar_init(bar(BAR_DM), 1);
@@ -213,51 +290,41 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   };
 
   if (warp < 4) {
-    // ------------------------------------------------ rows of y: t = tid
+    // ------------------------------------------------ P: row t = tid
     const int t = tid;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const float D = a.D ? a.D[h] : 0.0f;
-    const float2 D2 = make_float2(D, D);
-    const int pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;  // columns that exist
-    __nv_bfloat16* const yp = static_cast<__nv_bfloat16*>(a.y) + (size_t)h * a.P + p0;
-    const __nv_bfloat16* const zp =
-        a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)h * a.P + p0 : nullptr;
     for (int c = 0; c < nb; ++c) {
-      if (!wait(BAR_PREP + (c & 1), c >> 1) || !wait(BAR_S, c)) break;
+      const uint32_t stage = c & 1;
+      if (!wait(BAR_PREP + stage, c >> 1) || !wait(BAR_S + stage, c >> 1)) break;
       tc_fence_after();
-      float decay;  // from the block's start up to t
       const SsmPrep& pr = *prep(c);
+      const uint32_t sbuf = tm + TM_S + stage * 128 + lanes;
       const float in_t = pr.in[t];
-      // decay from the end of each earlier run up to t
-      float to[4];
-      {
-        float e = in_t;
+      float e = in_t;  // log2 decay from the end of run j up to t, j from warp - 1 down
+      float to[3];
 #pragma unroll
-        for (int j = 3; j >= 0; --j) {
-          to[j] = 0.0f;
-          if (j < warp) {
-            to[j] = fast_exp2(e);
-            e += pr.run[j];
-          }
+      for (int j = 2; j >= 0; --j) {
+        to[j] = 0.0f;
+        if (j < warp) {
+          to[j] = fast_exp2(e);
+          e += pr.run[j];
         }
-        decay = fast_exp2(e);
       }
-      const uint32_t sbuf = tm + TM_S + lanes;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t pk[16];
-        if (j > warp) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = 0u;
-        } else {
-          float s[32];
-          tmem_ld32(sbuf + 32 * j, s);
-          tmem_wait_ld();
+#pragma unroll 1
+      for (int grp = 0; grp < 8; ++grp) {  // 16 columns each
+        const int j = grp >> 1;
+        uint32_t pk[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (j <= warp) {
+          float s[16];
+          tmem_ld16(sbuf + 16 * grp, s);
           if (j < warp) {
-            const float2 f2 = make_float2(to[j], to[j]);
+            const float f = j == 0 ? to[0] : j == 1 ? to[1] : to[2];
+            const float2 f2 = make_float2(f, f);
+            const float4* o4 = reinterpret_cast<const float4*>(&pr.out[16 * grp]);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 o = *reinterpret_cast<const float4*>(&pr.out[32 * j + 4 * i]);
+            for (int i = 0; i < 4; ++i) {
+              const float4 o = o4[i];
               const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
                                     make_float2(s[4 * i], s[4 * i + 1]));
               const float2 v = mul2(mul2(make_float2(o.z, o.w), f2),
@@ -266,167 +333,210 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
               pk[2 * i + 1] = pack_bf16(v.x, v.y);
             }
           } else {
+            const float4* in4 = reinterpret_cast<const float4*>(&pr.in[16 * grp]);
+            const float4* d4 = reinterpret_cast<const float4*>(&pr.d[16 * grp]);
+            const int upto = t - 16 * grp;  // the row's own column in this group
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 in = *reinterpret_cast<const float4*>(&pr.in[32 * j + 4 * i]);
-              const float4 d = *reinterpret_cast<const float4*>(&pr.d[32 * j + 4 * i]);
+            for (int i = 0; i < 4; ++i) {
+              const float4 in = in4[i], d = d4[i];
               float w[4] = {s[4 * i] * d.x * fast_exp2(in_t - in.x),
                             s[4 * i + 1] * d.y * fast_exp2(in_t - in.y),
                             s[4 * i + 2] * d.z * fast_exp2(in_t - in.z),
                             s[4 * i + 3] * d.w * fast_exp2(in_t - in.w)};
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (4 * i + e > lane) w[e] = 0.0f;
+              for (int x = 0; x < 4; ++x)
+                if (4 * i + x > upto) w[x] = 0.0f;
               pk[2 * i] = pack_bf16(w[0], w[1]);
               pk[2 * i + 1] = pack_bf16(w[2], w[3]);
             }
           }
         }
-        // P's columns 16 j .. lie in columns of S that are already read
-        tmem_st16(sbuf + 16 * j, pk);
+        // P's columns 8 grp .. lie in columns of S that are already read
+        tmem_st8(sbuf + 8 * grp, pk);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(BAR_P));
-        mbar_arrive(bar(BAR_PREPFREE + (c & 1)));
-      }
-      const long long first = row0 + (long long)c * SB_L, row = first + t;
-      const bool live = row < row1, whole = first + SB_L <= row1;
-      uint4 zz[8];
-      if (zp) {  // on its way while the products finish
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (live && 8 * i < pn)
-            zz[i] = *reinterpret_cast<const uint4*>(zp + row * a.gate_stride + 8 * i);
-      }
-      if (!wait(BAR_Y2, c) || !wait(BAR_Y, c)) break;
-      tc_fence_after();
-      uint8_t* vtile = sm + SB_V + (c & 1) * SB_PANEL;
-      const float2 f2 = make_float2(decay, decay);
-#pragma unroll
-      for (int part = 0; part < 4; ++part) {
-        float y1[16], y2[16], y3[16];
-        tmem_ld16(tm + TM_Y1 + 16 * part + lanes, y1);
-        tmem_ld16(tm + TM_Y2 + 16 * part + lanes, y2);
-        tmem_ld16(tm + TM_Y2 + 64 + 16 * part + lanes, y3);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int ch = 2 * part + i;
-          uint4* place = reinterpret_cast<uint4*>(vtile + tile_offset(t, ch));
-          const uint4 vv = *place;
-          const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
-          float2 o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 8 * i + 2 * j;
-            const float2 r = fma2(f2, make_float2(y3[e], y3[e + 1]),
-                                  fma2(f2, make_float2(y2[e], y2[e + 1]),
-                                       make_float2(y1[e], y1[e + 1])));
-            o[j] = fma2(D2, unpack_bf16(vw[j]), r);
-          }
-          if (zp) {
-            const uint32_t zw[4] = {zz[ch].x, zz[ch].y, zz[ch].z, zz[ch].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 z = unpack_bf16(zw[j]);
-              o[j] = mul2(o[j], make_float2(fast_gate_act(z.x, a.act), fast_gate_act(z.y, a.act)));
-            }
-          }
-          const uint4 out = make_uint4(pack_bf16(o[0].x, o[0].y), pack_bf16(o[1].x, o[1].y),
-                                       pack_bf16(o[2].x, o[2].y), pack_bf16(o[3].x, o[3].y));
-          if (whole)
-            *place = out;  // v's last reader leaves y in its place
-          else if (live && 8 * ch < pn)
-            *reinterpret_cast<uint4*>(yp + (size_t)row * a.H * a.P + 8 * ch) = out;
-        }
-      }
-      if (whole) fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(BAR_Y2FREE));
-        if (whole) {
-          tma_store_3d(&ba.my, p0, h, (int)first + 32 * warp,
-                       base + SB_V + (c & 1) * SB_PANEL + warp * 4096);
-          tma_store_commit();
-          tma_store_wait_read();
-        }
-        mbar_arrive(bar(BAR_VFREE + (c & 1)));
+        mbar_arrive(bar(BAR_P + stage));
+        mbar_arrive(bar(BAR_PREPFREE + stage));
       }
     }
   } else if (warp < 8) {
-    // ------------------------------------------------ the state: row n = tid - 128
-    const int n = tid - 128;
-    const uint32_t lanes = (uint32_t)((warp - 4) * 32) << 16;
+    // ------------------------------------------------ Y: row t = tid - 128
+    const int t = tid - 128, quad = warp - 4;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const float D = a.D ? a.D[h] : 0.0f;
+    const float2 D2 = make_float2(D, D);
+    const int pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;  // columns that exist
+    __nv_bfloat16* const yp = static_cast<__nv_bfloat16*>(a.y) + (size_t)h * a.P + p0;
+    const __nv_bfloat16* const zp =
+        a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)h * a.P + p0 : nullptr;
+    // whole sectors where rows start on them and hold a multiple of 16 values
+    const bool sectors = a.P % 16 == 0 && a.gate_stride % 16 == 0 &&
+                         ((reinterpret_cast<uintptr_t>(yp) | reinterpret_cast<uintptr_t>(zp)) & 31) == 0;
+    for (int c = 0; c < nb; ++c) {
+      const uint32_t stage = c & 1;
+      const long long row = row0 + (long long)c * SB_L + t;
+      const bool live = row < row1;
+      const __nv_bfloat16* const zrow = zp + row * a.gate_stride;
+      __nv_bfloat16* const yrow = yp + (size_t)row * a.H * a.P;
+      if (!wait(BAR_PREP + stage, c >> 1) || !wait(BAR_VFULL + stage, c >> 1)) break;
+      float decay;  // from the block's start up to t
+      {
+        const SsmPrep& pr = *prep(c);
+        float e = pr.in[t];
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (j < quad) e += pr.run[j];
+        decay = fast_exp2(e);
+      }
+      const float2 f2 = make_float2(decay, decay);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + stage));
+      uint32_t z[8];
+      auto load_z = [&](int part) {
+        if (!zp || !live || 16 * part >= pn) return;
+        if (sectors) {
+          load_sector(zrow + 16 * part, z);
+        } else {
+          *reinterpret_cast<uint4*>(z) = *reinterpret_cast<const uint4*>(zrow + 16 * part);
+          if (16 * part + 8 < pn)
+            *reinterpret_cast<uint4*>(z + 4) = *reinterpret_cast<const uint4*>(zrow + 16 * part + 8);
+        }
+      };
+      load_z(0);  // on its way while the products finish
+      if (!wait(BAR_Y2, c) || !wait(BAR_Y + stage, c >> 1)) break;
+      tc_fence_after();
+      const uint8_t* vtile = sm + SB_V + stage * SB_PANEL;
+      const uint32_t ybuf = tm + TM_S + stage * 128 + TM_Y1 + lanes, y2buf = tm + TM_Y2 + lanes;
+#pragma unroll 1
+      for (int part = 0; part < 4; ++part) {
+        float y1[16], y2[16], y3[16];
+        tmem_ld16(ybuf + 16 * part, y1);
+        tmem_ld16(y2buf + 16 * part, y2);
+        tmem_ld16(y2buf + 64 + 16 * part, y3);
+        const uint4 va = *reinterpret_cast<const uint4*>(vtile + tile_offset(t, 2 * part)),
+                    vb = *reinterpret_cast<const uint4*>(vtile + tile_offset(t, 2 * part + 1));
+        const uint32_t vw[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+        float2 o[8];
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 r = add2(make_float2(y2[2 * j], y2[2 * j + 1]),
+                                make_float2(y3[2 * j], y3[2 * j + 1]));
+          o[j] = fma2(D2, unpack_bf16(vw[j]),
+                      fma2(f2, r, make_float2(y1[2 * j], y1[2 * j + 1])));
+        }
+        if (zp) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 g = unpack_bf16(z[j]);
+            o[j] = mul2(o[j], make_float2(fast_gate_act(g.x, a.act), fast_gate_act(g.y, a.act)));
+          }
+          if (part < 3) load_z(part + 1);
+        }
+        uint32_t out[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = pack_bf16(o[j].x, o[j].y);
+        if (live && 16 * part < pn) {
+          if (sectors) {
+            store_sector(yrow + 16 * part, out);
+          } else {
+            *reinterpret_cast<uint4*>(yrow + 16 * part) = make_uint4(out[0], out[1], out[2], out[3]);
+            if (16 * part + 8 < pn)
+              *reinterpret_cast<uint4*>(yrow + 16 * part + 8) =
+                  make_uint4(out[4], out[5], out[6], out[7]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(BAR_YFREE));
+        mbar_arrive(bar(BAR_Y2FREE));
+        mbar_arrive(bar(BAR_VFREE + stage));
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------ H: row n = tid - 256
+    const int n = tid - 256;
+    const uint32_t lanes = (uint32_t)((warp - 8) * 32) << 16;
     const int pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;
     float* const mrow = Mp + (size_t)n * a.P + p0;
+    const bool split = seq1 - seq0 > seg_rows;
+    const float* const from =
+        split ? ba.starts + (((size_t)item * a.H + h) * a.N + n) * a.P + p0 : mrow;
     float st[SB_P];
 #pragma unroll
     for (int i = 0; i < SB_P; i += 4) {
       float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!a.from_zero && n < a.N && i < pn) m = *reinterpret_cast<const float4*>(mrow + i);
+      if ((split || !a.from_zero) && n < a.N && i < pn)
+        m = *reinterpret_cast<const float4*>(from + i);
       st[i] = m.x;
       st[i + 1] = m.y;
       st[i + 2] = m.z;
       st[i + 3] = m.w;
     }
-    // two bf16 parts of the state row, as rows of the B operand of Y2
-    auto publish = [&]() {
-      uint8_t* hi = sm + SB_H;
-      uint8_t* lo = sm + SB_H + SB_PANEL;
+    // two bf16 parts of eight of the row's values, as a chunk of the B operand of Y2
+    auto publish = [&](int ch) {
+      uint32_t u[4], v[4];
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
-        uint32_t u[4], v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x0 = st[8 * ch + 2 * j], x1 = st[8 * ch + 2 * j + 1];
-          u[j] = pack_bf16(x0, x1);
-          const float2 r = unpack_bf16(u[j]);
-          v[j] = pack_bf16(x0 - r.x, x1 - r.y);
-        }
-        const uint32_t o = tile_offset(n, ch);
-        *reinterpret_cast<uint4*>(hi + o) = make_uint4(u[0], u[1], u[2], u[3]);
-        *reinterpret_cast<uint4*>(lo + o) = make_uint4(v[0], v[1], v[2], v[3]);
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = make_float2(st[8 * ch + 2 * j], st[8 * ch + 2 * j + 1]);
+        u[j] = pack_bf16(x.x, x.y);
+        const float2 r = sub2(x, unpack_bf16(u[j]));
+        v[j] = pack_bf16(r.x, r.y);
       }
+      uint8_t* place = sm + SB_H + tile_offset(n, ch);
+      *reinterpret_cast<uint4*>(place) = make_uint4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<uint4*>(place + SB_PANEL) = make_uint4(v[0], v[1], v[2], v[3]);
+    };
+    auto published = [&]() {
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_HREADY));
     };
-    publish();
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) publish(ch);
+    published();
     bool ok = true;
     for (int c = 0; c < nb; ++c) {
       ok = wait(BAR_PREP + (c & 1), c >> 1);
       if (!ok) break;
       const SsmPrep& pr = *prep(c);
       const float keep = exp2f((pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]));
+      const float2 keep2 = make_float2(keep, keep);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 1)));
-      ok = wait(BAR_DM, c);
+      ok = wait(BAR_DM, c) && wait(BAR_HFREE, c);
       if (!ok) break;
       tc_fence_after();
+      const bool more = c + 1 < nb;
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
-        float r1[16], r2[16], r3[16];
+        float r1[16], r2[16];
         tmem_ld16(tm + TM_DM + 16 * part + lanes, r1);
         tmem_ld16(tm + TM_DM + 64 + 16 * part + lanes, r2);
-        tmem_ld16(tm + TM_DM + 128 + 16 * part + lanes, r3);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          st[16 * part + i] = fmaf(st[16 * part + i], keep, r1[i] + (r2[i] + r3[i]));
+        for (int i = 0; i < 16; i += 2) {
+          const float2 x = fma2(make_float2(st[16 * part + i], st[16 * part + i + 1]), keep2,
+                                add2(make_float2(r1[i], r1[i + 1]), make_float2(r2[i], r2[i + 1])));
+          st[16 * part + i] = x.x;
+          st[16 * part + i + 1] = x.y;
+        }
+        if (more) {
+          publish(2 * part);
+          publish(2 * part + 1);
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_DMFREE));
-      if (c + 1 < nb) {
-        ok = wait(BAR_HFREE, c);
-        if (!ok) break;
-        publish();
-      }
+      if (more) published();
     }
     if (ok && row1 == seq1 && n < a.N) {
 #pragma unroll
@@ -435,108 +545,91 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           *reinterpret_cast<float4*>(mrow + i) =
               make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
     }
-  } else if (warp < 12) {
-    // ------------------------------------------------ w o v in three bf16 parts
-    const int i0 = tid - 256, rq = i0 >> 2;  // row in the quarter, and 16 of its values
+  } else if (warp < 16) {
+    // ------------------------------------------------ W: three bf16 parts of w o v
+    const int i0 = tid - 384, rq = i0 >> 2;  // row in the quarter, and 16 of its values
+    const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
     for (int c = 0; c < nb; ++c) {
       const int stage = c & 1;
       if (!wait(BAR_PREP + stage, c >> 1) || !wait(BAR_VFULL + stage, c >> 1)) break;
       uint8_t* vtile = sm + SB_V + stage * SB_PANEL;
+      const float* w = prep(c)->w;
       const long long left = row1 - (row0 + (long long)c * SB_L);
-      uint4 vv[8];
-      float w[4];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        vv[i] = *reinterpret_cast<const uint4*>(
-            vtile + tile_offset(32 * (i >> 1) + rq, 2 * (i0 & 3) + (i & 1)));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = prep(c)->w[32 * i + rq];
       if (left < SB_L) {
         // rows behind the segment's end, whatever they hold, become zeros
         if (!wait(BAR_KFULL + stage, c >> 1)) break;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int t = 32 * (i >> 1) + rq;
+        for (int t = rq; t < SB_L; t += 32) {
           if (t < left) continue;
-          const uint32_t o = tile_offset(t, 2 * (i0 & 3) + (i & 1));
-          vv[i] = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(vtile + o) = vv[i];
-          for (int pl = 0; pl < npanels; ++pl)
-            *reinterpret_cast<uint4*>(sm + SB_K + (2 * stage + pl) * SB_PANEL + o) = vv[i];
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t o = (i ? o1 : o0) + (t - rq) * 128;
+            *reinterpret_cast<uint4*>(vtile + o) = make_uint4(0, 0, 0, 0);
+            for (int pl = 0; pl < npanels; ++pl)
+              *reinterpret_cast<uint4*>(sm + SB_K + (2 * stage + pl) * SB_PANEL + o) =
+                  make_uint4(0, 0, 0, 0);
+          }
         }
       }
       bool ok = true;
-#pragma unroll
+#pragma unroll 1
       for (int qd = 0; qd < 4; ++qd) {
         const int use = 4 * c + qd, buf = qd & 1;
+        const uint4 va = *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o0),
+                    vb = *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o1);
         uint32_t p[3][8];
-        const float2 w2 = make_float2(w[qd], w[qd]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 u = vv[2 * qd + (j >> 2)];
-          const uint32_t word = (j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w;
-          float2 x = mul2(unpack_bf16(word), w2);
-          p[0][j] = pack_bf16(x.x, x.y);
-          x = sub2(x, unpack_bf16(p[0][j]));
-          p[1][j] = pack_bf16(x.x, x.y);
-          x = sub2(x, unpack_bf16(p[1][j]));
-          p[2][j] = pack_bf16(x.x, x.y);
-        }
-        ok = ok && (use < 2 || wait(BAR_WFREE + buf, (use >> 1) - 1));
-        uint8_t* wt = sm + SB_W + buf * 3 * SB_WPART;
-#pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<uint4*>(wt + part * SB_WPART + tile_offset(rq, 2 * (i0 & 3) + i)) =
-                make_uint4(p[part][4 * i], p[part][4 * i + 1], p[part][4 * i + 2],
-                           p[part][4 * i + 3]);
+        ssm_parts(va, vb, w[32 * qd + rq], p);
+        ok = use < 2 || wait(BAR_WFREE + buf, (use >> 1) - 1);
+        if (!ok) break;
+        ssm_store_parts(sm + SB_W + buf * 3 * SB_WPART, o0, o1, p);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_WREADY + buf));
       }
+      if (!ok) break;
       if (lane == 0) {
         mbar_arrive(bar(BAR_CLEAN + stage));
         mbar_arrive(bar(BAR_PREPFREE + stage));
       }
-      if (!ok) break;
     }
-  } else if (warp == 12) {
+  } else if (warp >= 16) {
+  if (warp == 16) {
     // ------------------------------------------------ products S and Y1
     constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY1 = mma_desc(128, 64, 0, 1);
     const uint32_t q0 = tile_desc(base + SB_Q), k0 = tile_desc(base + SB_K),
                    v0 = tile_desc(base + SB_V);
     for (int c = 0; c <= nb; ++c) {
-      if (c > 0) {
-        const int e = c - 1;
-        const uint32_t stage = e & 1;
-        if (!wait(BAR_CLEAN + stage, e >> 1) || !wait(BAR_VFULL + stage, e >> 1) ||
-            !wait(BAR_P, e))
-          break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t v = v0 + stage * (SB_PANEL >> 4);
-#pragma unroll
-          for (int i = 0; i < SB_L / 16; ++i)
-            mma_ts(tm + TM_Y1, tm + TM_S + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
-          mma_commit(bar(BAR_Y));
-        }
-        __syncwarp();
-      }
       if (c < nb) {
         const uint32_t stage = c & 1;
-        if (!wait(BAR_QFULL + stage, c >> 1) || !wait(BAR_KFULL + stage, c >> 1)) break;
+        if (!wait(BAR_QFULL + stage, c >> 1) || !wait(BAR_KFULL + stage, c >> 1) ||
+            (c >= 2 && !wait(BAR_YFREE, c - 2)))
+          break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t q = q0 + stage * (2 * SB_PANEL >> 4), k = k0 + stage * (2 * SB_PANEL >> 4);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t o = ((i >> 2) * SB_PANEL + (i & 3) * 32) >> 4;
-            if (i < nk) mma_ss(tm + TM_S, q + o, k + o, dS, i > 0);
+            if (i < nk) mma_ss(tm + TM_S + stage * 128, q + o, k + o, dS, i > 0);
           }
-          mma_commit(bar(BAR_S));
+          mma_commit(bar(BAR_S + stage));
           mma_commit(bar(BAR_KFREE + stage));
           mma_commit(bar(BAR_QFREE + stage));
+        }
+        __syncwarp();
+      }
+      if (c > 0) {
+        const int e = c - 1;
+        const uint32_t stage = e & 1;
+        if (!wait(BAR_CLEAN + stage, e >> 1) || !wait(BAR_VFULL + stage, e >> 1) ||
+            !wait(BAR_P + stage, e >> 1))
+          break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t v = v0 + stage * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
+#pragma unroll
+          for (int i = 0; i < SB_L / 16; ++i)
+            mma_ts(s + TM_Y1, s + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
+          mma_commit(bar(BAR_Y + stage));
+          mma_commit(bar(BAR_VFREE + stage));
         }
         __syncwarp();
       }
@@ -544,9 +637,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     if (elect_one()) mma_commit(bar(BAR_DRAIN));
     __syncwarp();
     mbar_wait(bar(BAR_DRAIN), 0, abort);
-  } else if (warp == 13) {
-    // ------------------------------------------------ product dM
-    constexpr uint32_t dM = mma_desc(128, 192, 1, 1);
+  } else if (warp == 17) {
+    // ------------------------------------------------ product dM: parts 0 | 1, part 2 onto 0
+    constexpr uint32_t dM = mma_desc(128, 128, 1, 1), dM2 = mma_desc(128, 64, 1, 1);
     const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W, SB_WPART);
     bool ok = true;
     for (int c = 0; c < nb && ok; ++c) {
@@ -560,8 +653,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (elect_one()) {
           const uint32_t kq = k + qd * (4096 >> 4), w = w0 + buf * (3 * SB_WPART >> 4);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) {
             mma_ss(tm + TM_DM, kq + i * (2048 >> 4), w + i * (2048 >> 4), dM, qd + i > 0);
+            mma_ss(tm + TM_DM, kq + i * (2048 >> 4), w + ((2 * SB_WPART + i * 2048) >> 4), dM2, true);
+          }
           mma_commit(bar(BAR_WFREE + buf));
           if (qd == 3) {
             mma_commit(bar(BAR_DM));
@@ -574,7 +669,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     if (elect_one()) mma_commit(bar(BAR_DRAIN + 1));
     __syncwarp();
     mbar_wait(bar(BAR_DRAIN + 1), 0, abort);
-  } else if (warp == 14) {
+  } else if (warp == 18) {
     // ------------------------------------------------ loads: each tile as soon as its place is free
     if (lane == 0) {
       int kc = 0, vc = 0, qc = 0;  // blocks whose load is issued
@@ -640,65 +735,34 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
     const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
     float raw[4];
+    auto row_of = [&](int c, int i) { return row0 + (long long)c * SB_L + 4 * lane + i; };
     auto fetch = [&](int c) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long r = row0 + (long long)c * SB_L + 4 * lane + i;
-        raw[i] = r < row1 ? __bfloat162float(dp[r * a.dt_stride]) : 0.0f;
-      }
+      for (int i = 0; i < 4; ++i)
+        raw[i] = row_of(c, i) < row1 ? __bfloat162float(dp[row_of(c, i) * a.dt_stride]) : 0.0f;
     };
     fetch(0);
     auto prepare = [&](int c) -> bool {
-      float d[4], la[4];
+      SsmSums o;
+      bool live[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long r = row0 + (long long)c * SB_L + 4 * lane + i;
-        d[i] = r < row1 ? ssm_step_size(raw[i] + bias, a.softplus) : 0.0f;
-        // 2^-160 is 0 in fp32: a stronger decay changes nothing and would cost the sums their
-        // low bits
-        la[i] = fmaxf(d[i] * A2, -160.0f);
-      }
+      for (int i = 0; i < 4; ++i) live[i] = row_of(c, i) < row1;
+      ssm_sums(raw, live, bias, A2, a.softplus, o);
       if (c + 1 < nb) fetch(c + 1);
-      // sums over the run's 8 lanes, from its start and from its end
-      const float own = (la[0] + la[1]) + (la[2] + la[3]);
-      float up = own, down = own;
-#pragma unroll
-      for (int s = 1; s < 8; s <<= 1) {
-        const float o = __shfl_up_sync(FULL_MASK, up, s, 8);
-        const float u = __shfl_down_sync(FULL_MASK, down, s, 8);
-        if ((lane & 7) >= s) up += o;
-        if ((lane & 7) + s < 8) down += u;
-      }
-      float before = __shfl_up_sync(FULL_MASK, up, 1, 8),
-            after = __shfl_down_sync(FULL_MASK, down, 1, 8);
-      if ((lane & 7) == 0) before = 0.0f;
-      if ((lane & 7) == 7) after = 0.0f;
-      float run[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) run[j] = __shfl_sync(FULL_MASK, up, 8 * j + 7);
-      float later = 0.0f;  // runs behind this lane's
-#pragma unroll
-      for (int j = 3; j >= 1; --j)
-        if (j > (lane >> 3)) later += run[j];
-      float in[4], out[4], w[4];
-      in[0] = before + la[0];
-      in[1] = before + (la[0] + la[1]);
-      in[2] = before + (la[0] + la[1] + la[2]);
-      in[3] = before + own;
-      const float tail[4] = {after + (la[1] + la[2] + la[3]), after + (la[2] + la[3]),
-                             after + la[3], after};
+      float out[4], w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        out[i] = d[i] * exp2f(tail[i]);
-        w[i] = d[i] * exp2f(tail[i] + later);
+        out[i] = o.d[i] * exp2f(o.tail[i]);
+        w[i] = o.d[i] * exp2f(o.tail[i] + o.later);
       }
       if (c >= 2 && !wait(BAR_PREPFREE + (c & 1), (c >> 1) - 1)) return false;
       SsmPrep* pr = prep(c);
-      reinterpret_cast<float4*>(pr->d)[lane] = make_float4(d[0], d[1], d[2], d[3]);
-      reinterpret_cast<float4*>(pr->in)[lane] = make_float4(in[0], in[1], in[2], in[3]);
+      reinterpret_cast<float4*>(pr->d)[lane] = make_float4(o.d[0], o.d[1], o.d[2], o.d[3]);
+      reinterpret_cast<float4*>(pr->in)[lane] = make_float4(o.in[0], o.in[1], o.in[2], o.in[3]);
       reinterpret_cast<float4*>(pr->out)[lane] = make_float4(out[0], out[1], out[2], out[3]);
       reinterpret_cast<float4*>(pr->w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
-      if (lane < 4) pr->run[lane] = lane == 0 ? run[0] : lane == 1 ? run[1] : lane == 2 ? run[2] : run[3];
+      if (lane < 4)
+        pr->run[lane] = lane == 0 ? o.run[0] : lane == 1 ? o.run[1] : lane == 2 ? o.run[2] : o.run[3];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_PREP + (c & 1)));
       return true;
@@ -730,10 +794,268 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     __syncwarp();
     mbar_wait(bar(BAR_DRAIN + 2), 0, abort);
   }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_free(tm, 512);
+}
+
+// ------------------------------------------------------------------------ split sequences
+// With few (sequence, head, tile) CTAs a sequence is cut into segments that are scanned at the
+// same time, each from the state before it.  Those states come from one more pass that makes
+// each segment's own contribution, dM over all its tokens at once (this kernel: one product,
+// no state to carry), and a short chain over the segments (ssm_chain_kernel).
+//
+// A segment's contribution is summed from its last block to its first, so that every token's
+// weight, its decay up to the segment's end, is known when its block is read, and all blocks
+// accumulate in the same tensor memory.
+//   warps 0-7  w o v in parts, two groups at alternate quarters
+//   warp 8 products, warp 9 loads, warp 10 step sizes and decay sums
+constexpr int SG_THREADS = 384;
+constexpr uint32_t SG_K = 0;                        // 2 stages x 2 panels
+constexpr uint32_t SG_V = SG_K + 4 * SB_PANEL;      // 2 stages
+constexpr uint32_t SG_W = SG_V + 2 * SB_PANEL;      // 4 quarters x 3 parts
+constexpr uint32_t SG_WT = SG_W + 12 * SB_WPART;    // 2 x 128 weights
+constexpr uint32_t SG_BARS = SG_WT + 2 * SB_L * 4;
+enum { GB_KVFULL = 0, GB_KVFREE = 2, GB_PREP = 4, GB_PREPFREE = 6, GB_WREADY = 8, GB_WFREE = 12,
+       GB_DONE = 16, GB_COUNT };
+constexpr uint32_t SG_TMEM_PTR = SG_BARS + 20 * 8;
+constexpr uint32_t SG_SMEM = SG_TMEM_PTR + 32 + 1024;
+
+__global__ void __launch_bounds__(SG_THREADS, 1)
+    ssm_segment_kernel(const __grid_constant__ SsmBlockArgs ba) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_abort, s_item_ok, s_b;
+  __shared__ long long s_seg;
+  const SsmArgs& a = ba.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const sm = smem_raw + (base - smem_addr(smem_raw));
+  const uint32_t bars = base + SG_BARS;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+
+  const int per_item = a.H * ba.ptiles;
+  const long long item = blockIdx.x / per_item;
+  const int hp = blockIdx.x % per_item, h = hp / ba.ptiles, p0 = hp % ba.ptiles * SB_P;
+  const int g = h / (a.H / a.G);
+  const long long seg_rows = (long long)ba.seg_blocks * SB_L;
+  if (warp == 0) {
+    int b = 0;
+    long long s = 0;
+    const bool ok = ssm_find_item(a.seq, item, seg_rows, &b, &s);
+    if (lane == 0) {
+      s_item_ok = ok;
+      s_b = b;
+      s_seg = s;
+      s_abort = 0;
+    }
+  }
+  __syncthreads();
+  if (!s_item_ok) return;
+  const long long row0 = a.seq.start(s_b) + s_seg * seg_rows;
+  if (row0 + seg_rows >= a.seq.end(s_b)) return;  // nothing follows the last segment
+  const int nb = ba.seg_blocks;                   // all whole
+  const int npanels = a.N > 64 ? 2 : 1;
+
+  if (warp == 0) tmem_alloc(base + SG_TMEM_PTR, 128);
+  if (tid == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(GB_KVFULL + i), 1);
+      mbar_init(bar(GB_KVFREE + i), 1);
+      mbar_init(bar(GB_PREP + i), 1);
+      mbar_init(bar(GB_PREPFREE + i), 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(GB_WREADY + i), 4);
+      mbar_init(bar(GB_WFREE + i), 1);
+    }
+    mbar_init(bar(GB_DONE), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (npanels == 1) {
+    uint4* z = reinterpret_cast<uint4*>(sm + SG_K);
+    for (int i = tid; i < 2 * (int)SB_PANEL / 16; i += SG_THREADS) {
+      const int stage = i / (SB_PANEL / 16), j = i % (SB_PANEL / 16);
+      z[(2 * stage + 1) * (SB_PANEL / 16) + j] = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + SG_TMEM_PTR);
+  volatile int* const abort = &s_abort;
+  auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u, abort); };
+  float* const weights = reinterpret_cast<float*>(sm + SG_WT);
+
+  if (warp < 8) {
+    const int grp = warp >> 2, i0 = tid & 127, rq = i0 >> 2;
+    const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
+    bool ok = true;
+    for (int c = 0; c < nb && ok; ++c) {
+      const int stage = c & 1;
+      ok = wait(GB_PREP + stage, c >> 1) && wait(GB_KVFULL + stage, c >> 1);
+      if (!ok) break;
+      const uint8_t* vtile = sm + SG_V + stage * SB_PANEL;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int qd = 2 * i + grp;  // the group's buffers: qd
+        uint32_t p[3][8];
+        ssm_parts(*reinterpret_cast<const uint4*>(vtile + 4096 * qd + o0),
+                  *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o1),
+                  weights[stage * SB_L + 32 * qd + rq], p);
+        ok = ok && (c == 0 || wait(GB_WFREE + qd, c - 1));
+        ssm_store_parts(sm + SG_W + qd * 3 * SB_WPART, o0, o1, p);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(GB_WREADY + qd));
+      }
+      if (lane == 0) mbar_arrive(bar(GB_PREPFREE + stage));
+    }
+    if (warp < 4 && ok && wait(GB_DONE, 0)) {
+      tc_fence_after();
+      const int n = tid, pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;
+      const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+      // the state before the next segment gets this one's contribution
+      float* to = ba.starts + (((size_t)(item + 1) * a.H + h) * a.N + n) * a.P + p0;
+#pragma unroll
+      for (int part = 0; part < 4; ++part) {
+        float r1[16], r2[16];
+        tmem_ld16(tm + 16 * part + lanes, r1);
+        tmem_ld16(tm + 64 + 16 * part + lanes, r2);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          if (n < a.N && 16 * part + i < pn)
+            *reinterpret_cast<float4*>(to + 16 * part + i) =
+                make_float4(r1[i] + r2[i], r1[i + 1] + r2[i + 1], r1[i + 2] + r2[i + 2],
+                            r1[i + 3] + r2[i + 3]);
+      }
+    }
+  } else if (warp == 8) {
+    constexpr uint32_t dM = mma_desc(128, 128, 1, 1), dM2 = mma_desc(128, 64, 1, 1);
+    const uint32_t k0 = tile_desc(base + SG_K, SB_PANEL), w0 = tile_desc(base + SG_W, SB_WPART);
+    bool ok = true;
+    for (int c = 0; c < nb && ok; ++c) {
+      const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
+      ok = wait(GB_KVFULL + stage, c >> 1);
+      for (int qd = 0; qd < 4 && ok; ++qd) {
+        ok = wait(GB_WREADY + qd, c);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t kq = k + qd * (4096 >> 4), w = w0 + qd * (3 * SB_WPART >> 4);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma_ss(tm, kq + i * (2048 >> 4), w + i * (2048 >> 4), dM, c + qd + i > 0);
+            mma_ss(tm, kq + i * (2048 >> 4), w + ((2 * SB_WPART + i * 2048) >> 4), dM2, true);
+          }
+          mma_commit(bar(GB_WFREE + qd));
+          if (qd == 3) mma_commit(bar(GB_KVFREE + stage));
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) mma_commit(bar(GB_DONE));
+    __syncwarp();
+    mbar_wait(bar(GB_DONE), 0, abort);
+  } else if (warp == 9) {
+    if (lane == 0) {
+      int c = 0;
+      for (; c < nb; ++c) {
+        const uint32_t stage = c & 1;
+        const int r = (int)(row0 + (long long)(nb - 1 - c) * SB_L);
+        if (c >= 2 && !wait(GB_KVFREE + stage, (c >> 1) - 1)) break;
+        mbar_expect(bar(GB_KVFULL + stage), (npanels + 1) * SB_PANEL);
+        tma_load_3d(base + SG_V + stage * SB_PANEL, &ba.mv, p0, h, r, bar(GB_KVFULL + stage));
+        for (int pl = 0; pl < npanels; ++pl)
+          tma_load_3d(base + SG_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
+                      bar(GB_KVFULL + stage));
+      }
+      if (*abort) {
+        int none = 0;
+        for (int e = c > 2 ? c - 2 : 0; e < c; ++e)
+          mbar_wait(bar(GB_KVFULL + (e & 1)), (uint32_t)(e >> 1) & 1u, &none);
+      }
+    }
+  } else if (warp == 10) {
+    const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
+    const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+    float raw[4], carry = 0.0f;  // log2 decay of the blocks behind
+    const bool live[4] = {true, true, true, true};
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        raw[i] = __bfloat162float(
+            dp[(row0 + (long long)(nb - 1 - c) * SB_L + 4 * lane + i) * a.dt_stride]);
+    };
+    fetch(0);
+    for (int c = 0; c < nb; ++c) {
+      SsmSums o;
+      ssm_sums(raw, live, bias, A2, a.softplus, o);
+      if (c + 1 < nb) fetch(c + 1);
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = o.d[i] * exp2f((o.tail[i] + o.later) + carry);
+      carry += (o.run[0] + o.run[1]) + (o.run[2] + o.run[3]);
+      if (c >= 2 && !wait(GB_PREPFREE + (c & 1), (c >> 1) - 1)) break;
+      reinterpret_cast<float4*>(weights + (c & 1) * SB_L)[lane] =
+          make_float4(w[0], w[1], w[2], w[3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(GB_PREP + (c & 1)));
+    }
+    if (lane == 0 && p0 == 0) ba.decays[item * a.H + h] = exp2f(carry);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_free(tm, 128);
+}
+
+// The states before the segments of a split sequence, from the first on: what the sequence
+// starts with, then each segment's decay and contribution.  A block per (sequence, head, 1024
+// state values).
+__global__ void __launch_bounds__(256) ssm_chain_kernel(const __grid_constant__ SsmBlockArgs ba) {
+  __shared__ long long s_first;
+  const SsmArgs& a = ba.a;
+  const int b = blockIdx.x, h = blockIdx.y, i = blockIdx.z * 256 + threadIdx.x;
+  const long long seg = (long long)ba.seg_blocks * SB_L, len = a.seq.end(b) - a.seq.start(b);
+  if (len <= seg) return;
+  if (threadIdx.x == 0) s_first = 0;
+  __syncthreads();
+  if (!a.seq.cu) {
+    if (threadIdx.x == 0) s_first = b * ((a.seq.T + seg - 1) / seg);
+  } else {
+    long long items = 0;
+    for (int e = threadIdx.x; e < b; e += 256) {
+      const long long n = a.seq.end(e) - a.seq.start(e);
+      items += n > 0 ? (n + seg - 1) / seg : 1;
+    }
+    if (items)
+      atomicAdd(reinterpret_cast<unsigned long long*>(&s_first), (unsigned long long)items);
+  }
+  __syncthreads();
+  const int n4 = a.N * a.P / 4;
+  if (i >= n4) return;
+  const long long first = s_first;
+  const int segs = (int)((len + seg - 1) / seg);
+  const size_t step = (size_t)a.H * n4;
+  float4* at = reinterpret_cast<float4*>(ba.starts) + ((size_t)first * a.H + h) * n4 + i;
+  const float* decay = ba.decays + first * a.H + h;
+  float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!a.from_zero) m = reinterpret_cast<const float4*>(a.M)[((size_t)b * a.H + h) * n4 + i];
+  at[0] = m;
+#pragma unroll 4
+  for (int s = 1; s < segs; ++s) {
+    const float4 e = at[s * step];
+    const float f = decay[(size_t)(s - 1) * a.H];
+    m.x = fmaf(m.x, f, e.x);
+    m.y = fmaf(m.y, f, e.y);
+    m.z = fmaf(m.z, f, e.z);
+    m.w = fmaf(m.w, f, e.w);
+    at[s * step] = m;
+  }
 }
 
 }  // namespace sdm

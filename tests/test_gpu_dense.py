@@ -199,6 +199,35 @@ def test_ssm_packed(sdm, dt, lens, init):
     assert (y[:before] == 7).all() and (y[before + n:] == 7).all()
 
 
+@pytest.mark.parametrize("B,T,H,N,P,init", [
+    (1, 5000, 2, 128, 64, "continue"), (2, 2437, 3, 64, 128, "zero"), (1, 4096, 1, 16, 40, "continue"),
+])
+def test_ssm_long(sdm, B, T, H, N, P, init):
+    """Prompts that are cut into segments (few heads, many blocks)."""
+    i, M = ssm_inputs(gen(T), (B, T), H, 1, N, P, torch.bfloat16, True, True, B)
+    M0 = d64(M) if init == "continue" else torch.zeros_like(d64(M))
+    y = sdm.sdm_ssm_forward(M=M, init=init, **i)
+    ry, rM, yb, Mb = ssm_ref(i, M0, [T] * B, "bf16")
+    ref.check(y.reshape(B * T, H, P), ry, yb, "y")
+    ref.check(M, rM, Mb, "M")
+
+
+@pytest.mark.parametrize("init", ["zero", "continue"])
+@pytest.mark.parametrize("lens", [[3000, 1, 0, 700, 1280, 128, 129], [0, 6000]])
+def test_ssm_long_packed(sdm, lens, init):
+    """Packed batches with sequences of several segments next to short and empty ones."""
+    B, H, N, P, n = len(lens), 2, 128, 64, sum(lens)
+    i, M = ssm_inputs(gen(n), (n + 3,), H, 2, N, P, torch.bfloat16, True, True, B)
+    M0 = d64(M) if init == "continue" else torch.zeros_like(d64(M))
+    y = torch.full_like(i["v"], 7.0)
+    sdm.sdm_ssm_forward(M=M, init=init, cu=cu_of(lens), y=y, **i)
+    own = {x: (z[:n] if x in ("k", "q", "v", "dt", "gate") else z) for x, z in i.items()}
+    ry, rM, yb, Mb = ssm_ref(own, M0, lens, "bf16")
+    ref.check(y[:n], ry, yb, "y")
+    ref.check(M, rM, Mb, "M")
+    assert (y[n:] == 7).all()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_ssm_views_of_one_row(sdm, dt):
     """k, q, v, dt and the gate as slices of one projected row give the bits of copies."""
