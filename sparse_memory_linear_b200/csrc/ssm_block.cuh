@@ -8,10 +8,9 @@
 //   S  = q k^T                      128 x 128 x N
 //   Y2 = q M                        128 x (2 x 64) x N, M as two bf16 parts (16 bits of it)
 //   Y1 = (S o weights) v            128 x 64 x 128, weights rounded to bf16
-//   dM = k^T (w o v)                N x (2 x 64) x 128 and N x 64 x 128, w o v as three bf16
-//                                   parts (24 bits)
-// The parts lie side by side as columns of one product, so that q and k are read from shared
-// memory once for all of them: its bandwidth is what the matrix unit waits for at these sizes.
+//   dM = k^T (w o v)                3 products N x 64 x 128, w o v as three bf16 parts (24 bits)
+// The parts of M lie side by side as columns of one product, so that q is read from shared
+// memory once for both.
 // The state is kept in fp32 registers and never rounded to less: dM has to be exact to fp32,
 // hence the three parts.  What enters y may be rounded to the type of y once: each token's
 // weight in another's read (half a step of bf16); two parts of M keep the second term below
@@ -23,8 +22,8 @@
 //   Y   a thread per token row: y = exp(c_t) Y2 + Y1 + D v, gated and stored
 //   H   a thread per state row: adds dM to the decayed state, publishes the state's two parts
 //   W   a thread per quarter row of v: w o v in parts, 32 tokens at a time
-//   and four single warps: S and Y1; dM; TMA loads of q, k, v; step sizes and decay sums two
-//   blocks ahead, with Y2
+//   and four single warps: step sizes and decay sums two blocks ahead, with Y2; dM; S and Y1;
+//   TMA loads
 // joined by mbarriers.  A block's work is a chain of short dependent steps; with the steps on
 // warps of their own the chains of successive blocks overlap.
 //
@@ -64,8 +63,8 @@ constexpr uint32_t SB_BARS = SB_PREP + 2 * sizeof(SsmPrep);
 enum {
   BAR_QFULL = 0, BAR_QFREE = 2, BAR_KFULL = 4, BAR_KFREE = 6, BAR_VFULL = 8, BAR_VFREE = 10,
   BAR_PREP = 12, BAR_PREPFREE = 14, BAR_WREADY = 16, BAR_WFREE = 18, BAR_CLEAN = 20,
-  BAR_S = 22, BAR_P = 24, BAR_Y = 26, BAR_YFREE = 28, BAR_Y2, BAR_Y2FREE, BAR_DM, BAR_DMFREE,
-  BAR_HREADY, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 3
+  BAR_S = 22, BAR_P = 24, BAR_Y = 26, BAR_DM = 28, BAR_DMFREE = 30, BAR_YFREE = 32, BAR_Y2,
+  BAR_Y2FREE, BAR_HREADY, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 3
 };
 constexpr uint32_t SB_TMEM_PTR = SB_BARS + 40 * 8;
 static_assert(BAR_COUNT <= 40, "barriers");
@@ -73,7 +72,7 @@ constexpr uint32_t SB_SMEM = SB_TMEM_PTR + 32 + 1024;      // and room to align
 static_assert(SB_SMEM <= 232448 - 64, "shared memory of a block");
 
 // Tensor memory columns: two buffers of S, whose first half becomes P and whose second half,
-// once weighed, holds Y1; Y2 and dM of one block.
+// once weighed, holds Y1; Y2's two parts; two buffers of dM.
 constexpr uint32_t TM_S = 0, TM_Y1 = 64, TM_Y2 = 256, TM_DM = 384;
 
 constexpr float SB_LOG2E = 1.4426950408889634f;
@@ -259,12 +258,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       mbar_init(bar(BAR_S + i), 1);
       mbar_init(bar(BAR_P + i), 4);
       mbar_init(bar(BAR_Y + i), 1);
+      mbar_init(bar(BAR_DM + i), 1);
+      mbar_init(bar(BAR_DMFREE + i), 4);
     }
     mbar_init(bar(BAR_YFREE), 4);
     mbar_init(bar(BAR_Y2), 1);
     mbar_init(bar(BAR_Y2FREE), 4);
-    mbar_init(bar(BAR_DM), 1);
-    mbar_init(bar(BAR_DMFREE), 4);
     mbar_init(bar(BAR_HREADY), 4);
     mbar_init(bar(BAR_HFREE), 1);
     for (int i = 0; i < 3; ++i) mbar_init(bar(BAR_DRAIN + i), 1);
@@ -311,49 +310,54 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         }
       }
 #pragma unroll 1
-      for (int grp = 0; grp < 8; ++grp) {  // 16 columns each
-        const int j = grp >> 1;
-        uint32_t pk[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (j <= warp) {
-          float s[16];
-          tmem_ld16(sbuf + 16 * grp, s);
-          if (j < warp) {
-            const float f = j == 0 ? to[0] : j == 1 ? to[1] : to[2];
-            const float2 f2 = make_float2(f, f);
-            const float4* o4 = reinterpret_cast<const float4*>(&pr.out[16 * grp]);
-            tmem_wait_ld();
+      for (int j = 0; j < 4; ++j) {  // runs of 32 columns
+        uint32_t pk[16];
+        if (j < warp) {
+          float s[32];
+          tmem_ld32(sbuf + 32 * j, s);
+          const float f = j == 0 ? to[0] : j == 1 ? to[1] : to[2];
+          const float2 f2 = make_float2(f, f);
+          const float4* o4 = reinterpret_cast<const float4*>(&pr.out[32 * j]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 o = o4[i];
-              const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
-                                    make_float2(s[4 * i], s[4 * i + 1]));
-              const float2 v = mul2(mul2(make_float2(o.z, o.w), f2),
-                                    make_float2(s[4 * i + 2], s[4 * i + 3]));
-              pk[2 * i] = pack_bf16(u.x, u.y);
-              pk[2 * i + 1] = pack_bf16(v.x, v.y);
-            }
-          } else {
-            const float4* in4 = reinterpret_cast<const float4*>(&pr.in[16 * grp]);
-            const float4* d4 = reinterpret_cast<const float4*>(&pr.d[16 * grp]);
-            const int upto = t - 16 * grp;  // the row's own column in this group
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 in = in4[i], d = d4[i];
-              float w[4] = {s[4 * i] * d.x * fast_exp2(in_t - in.x),
-                            s[4 * i + 1] * d.y * fast_exp2(in_t - in.y),
-                            s[4 * i + 2] * d.z * fast_exp2(in_t - in.z),
-                            s[4 * i + 3] * d.w * fast_exp2(in_t - in.w)};
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (4 * i + x > upto) w[x] = 0.0f;
-              pk[2 * i] = pack_bf16(w[0], w[1]);
-              pk[2 * i + 1] = pack_bf16(w[2], w[3]);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float4 o = o4[i];
+            const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
+                                  make_float2(s[4 * i], s[4 * i + 1]));
+            const float2 v = mul2(mul2(make_float2(o.z, o.w), f2),
+                                  make_float2(s[4 * i + 2], s[4 * i + 3]));
+            pk[2 * i] = pack_bf16(u.x, u.y);
+            pk[2 * i + 1] = pack_bf16(v.x, v.y);
           }
+        } else if (j == warp) {
+          float s[32];
+          tmem_ld32(sbuf + 32 * j, s);
+          const float4* in4 = reinterpret_cast<const float4*>(&pr.in[32 * j]);
+          const float4* d4 = reinterpret_cast<const float4*>(&pr.d[32 * j]);
+          const float2 t2 = make_float2(in_t, in_t);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 in = in4[i], d = d4[i];
+            const float2 e0 = sub2(t2, make_float2(in.x, in.y)),
+                         e1 = sub2(t2, make_float2(in.z, in.w));
+            float2 u = mul2(mul2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(d.x, d.y)),
+                            make_float2(fast_exp2(e0.x), fast_exp2(e0.y)));
+            float2 v = mul2(mul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(d.z, d.w)),
+                            make_float2(fast_exp2(e1.x), fast_exp2(e1.y)));
+            if (4 * i > lane) u.x = 0.0f;
+            if (4 * i + 1 > lane) u.y = 0.0f;
+            if (4 * i + 2 > lane) v.x = 0.0f;
+            if (4 * i + 3 > lane) v.y = 0.0f;
+            pk[2 * i] = pack_bf16(u.x, u.y);
+            pk[2 * i + 1] = pack_bf16(v.x, v.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = 0u;
         }
-        // P's columns 8 grp .. lie in columns of S that are already read
-        tmem_st8(sbuf + 8 * grp, pk);
+        // P's columns 16 j .. lie in columns of S that are already read
+        tmem_st16(sbuf + 16 * j, pk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -406,6 +410,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             *reinterpret_cast<uint4*>(z + 4) = *reinterpret_cast<const uint4*>(zrow + 16 * part + 8);
         }
       };
+      if (zp && row + 2 * SB_L < row1) prefetch_l2(zrow + 2 * SB_L * a.gate_stride);
       load_z(0);  // on its way while the products finish
       if (!wait(BAR_Y2, c) || !wait(BAR_Y + stage, c >> 1)) break;
       tc_fence_after();
@@ -468,23 +473,21 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const bool split = seq1 - seq0 > seg_rows;
     const float* const from =
         split ? ba.starts + (((size_t)item * a.H + h) * a.N + n) * a.P + p0 : mrow;
-    float st[SB_P];
+    float2 st[SB_P / 2];
 #pragma unroll
     for (int i = 0; i < SB_P; i += 4) {
       float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
       if ((split || !a.from_zero) && n < a.N && i < pn)
         m = *reinterpret_cast<const float4*>(from + i);
-      st[i] = m.x;
-      st[i + 1] = m.y;
-      st[i + 2] = m.z;
-      st[i + 3] = m.w;
+      st[i / 2] = make_float2(m.x, m.y);
+      st[i / 2 + 1] = make_float2(m.z, m.w);
     }
     // two bf16 parts of eight of the row's values, as a chunk of the B operand of Y2
     auto publish = [&](int ch) {
       uint32_t u[4], v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 x = make_float2(st[8 * ch + 2 * j], st[8 * ch + 2 * j + 1]);
+        const float2 x = st[4 * ch + j];
         u[j] = pack_bf16(x.x, x.y);
         const float2 r = sub2(x, unpack_bf16(u[j]));
         v[j] = pack_bf16(r.x, r.y);
@@ -508,42 +511,40 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       if (!ok) break;
       const SsmPrep& pr = *prep(c);
       const float keep = exp2f((pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]));
-      const float2 keep2 = make_float2(keep, keep);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 1)));
-      ok = wait(BAR_DM, c) && wait(BAR_HFREE, c);
+      ok = wait(BAR_DM + (c & 1), c >> 1);
       if (!ok) break;
       tc_fence_after();
-      const bool more = c + 1 < nb;
+      const uint32_t dm = tm + TM_DM + (c & 1) * 64 + lanes;
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
-        float r1[16], r2[16];
-        tmem_ld16(tm + TM_DM + 16 * part + lanes, r1);
-        tmem_ld16(tm + TM_DM + 64 + 16 * part + lanes, r2);
+        float r[16];
+        tmem_ld16(dm + 16 * part, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float2 x = fma2(make_float2(st[16 * part + i], st[16 * part + i + 1]), keep2,
-                                add2(make_float2(r1[i], r1[i + 1]), make_float2(r2[i], r2[i + 1])));
-          st[16 * part + i] = x.x;
-          st[16 * part + i + 1] = x.y;
-        }
-        if (more) {
-          publish(2 * part);
-          publish(2 * part + 1);
-        }
+        for (int i = 0; i < 8; ++i)
+          // one by one: as pairs the state would be held twice, and spilled
+          st[8 * part + i] = make_float2(fmaf(st[8 * part + i].x, keep, r[2 * i]),
+                                         fmaf(st[8 * part + i].y, keep, r[2 * i + 1]));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_DMFREE));
-      if (more) published();
+      if (lane == 0) mbar_arrive(bar(BAR_DMFREE + (c & 1)));
+      if (c + 1 < nb) {
+        ok = wait(BAR_HFREE, c);
+        if (!ok) break;
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) publish(ch);
+        published();
+      }
     }
     if (ok && row1 == seq1 && n < a.N) {
 #pragma unroll
       for (int i = 0; i < SB_P; i += 4)
         if (i < pn)
           *reinterpret_cast<float4*>(mrow + i) =
-              make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+              make_float4(st[i / 2].x, st[i / 2].y, st[i / 2 + 1].x, st[i / 2 + 1].y);
     }
   } else if (warp < 16) {
     // ------------------------------------------------ W: three bf16 parts of w o v
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
     }
   } else if (warp >= 16) {
-  if (warp == 16) {
+  if (warp == 18) {
     // ------------------------------------------------ products S and Y1
     constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY1 = mma_desc(128, 64, 0, 1);
     const uint32_t q0 = tile_desc(base + SB_Q), k0 = tile_desc(base + SB_K),
@@ -638,13 +639,14 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     __syncwarp();
     mbar_wait(bar(BAR_DRAIN), 0, abort);
   } else if (warp == 17) {
-    // ------------------------------------------------ product dM: parts 0 | 1, part 2 onto 0
-    constexpr uint32_t dM = mma_desc(128, 128, 1, 1), dM2 = mma_desc(128, 64, 1, 1);
-    const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W, SB_WPART);
+    // ------------------------------------------------ product dM, the parts onto one another
+    constexpr uint32_t dM = mma_desc(128, 64, 1, 1);
+    const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W);
     bool ok = true;
     for (int c = 0; c < nb && ok; ++c) {
       const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
-      ok = wait(BAR_KFULL + stage, c >> 1) && (c == 0 || wait(BAR_DMFREE, c - 1));
+      ok = wait(BAR_KFULL + stage, c >> 1) &&
+           (c < 2 || wait(BAR_DMFREE + stage, (c >> 1) - 1));
       for (int qd = 0; qd < 4 && ok; ++qd) {
         const uint32_t use = 4 * c + qd, buf = use & 1;
         ok = wait(BAR_WREADY + buf, use >> 1);
@@ -653,13 +655,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (elect_one()) {
           const uint32_t kq = k + qd * (4096 >> 4), w = w0 + buf * (3 * SB_WPART >> 4);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mma_ss(tm + TM_DM, kq + i * (2048 >> 4), w + i * (2048 >> 4), dM, qd + i > 0);
-            mma_ss(tm + TM_DM, kq + i * (2048 >> 4), w + ((2 * SB_WPART + i * 2048) >> 4), dM2, true);
-          }
+          for (int i = 0; i < 6; ++i)
+            mma_ss(tm + TM_DM + stage * 64, kq + (i & 1) * (2048 >> 4),
+                   w + (((i >> 1) * SB_WPART + (i & 1) * 2048) >> 4), dM, qd + i > 0);
           mma_commit(bar(BAR_WFREE + buf));
           if (qd == 3) {
-            mma_commit(bar(BAR_DM));
+            mma_commit(bar(BAR_DM + stage));
             mma_commit(bar(BAR_KFREE + stage));
           }
         }
@@ -669,25 +670,26 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     if (elect_one()) mma_commit(bar(BAR_DRAIN + 1));
     __syncwarp();
     mbar_wait(bar(BAR_DRAIN + 1), 0, abort);
-  } else if (warp == 18) {
+  } else if (warp == 19) {
     // ------------------------------------------------ loads: each tile as soon as its place is free
     if (lane == 0) {
       int kc = 0, vc = 0, qc = 0;  // blocks whose load is issued
       const int r0 = (int)row0;
       unsigned long long since = 0;
+      auto may = [&](int c, int free_bar) {
+        return c < nb &&
+               (c < 2 || mbar_test(bar(free_bar + (c & 1)), (uint32_t)((c >> 1) - 1) & 1u));
+      };
       while (kc < nb || vc < nb || qc < nb) {
         bool moved = false;
-        auto may = [&](int c, int free_bar) {
-          return c < nb &&
-                 (c < 2 || mbar_test(bar(free_bar + (c & 1)), (uint32_t)((c >> 1) - 1) & 1u));
-        };
-        if (may(qc, BAR_QFREE)) {
-          const uint32_t stage = qc & 1;
-          mbar_expect(bar(BAR_QFULL + stage), npanels * SB_PANEL);
-          for (int pl = 0; pl < npanels; ++pl)
-            tma_load_3d(base + SB_Q + (2 * stage + pl) * SB_PANEL, &ba.mq, 64 * pl, g,
-                        r0 + qc * SB_L, bar(BAR_QFULL + stage));
-          ++qc;
+        if (may(vc, BAR_VFREE)) {
+          const uint32_t stage = vc & 1;
+          mbar_expect(bar(BAR_VFULL + stage), SB_PANEL);
+          tma_load_3d(base + SB_V + stage * SB_PANEL, &ba.mv, p0, h, r0 + vc * SB_L,
+                      bar(BAR_VFULL + stage));
+          // two blocks ahead into L2: a load from memory takes longer than a block's work
+          if (vc + 2 < nb) tma_prefetch_3d(&ba.mv, p0, h, r0 + (vc + 2) * SB_L);
+          ++vc;
           moved = true;
         }
         if (may(kc, BAR_KFREE)) {
@@ -699,12 +701,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           ++kc;
           moved = true;
         }
-        if (may(vc, BAR_VFREE)) {
-          const uint32_t stage = vc & 1;
-          mbar_expect(bar(BAR_VFULL + stage), SB_PANEL);
-          tma_load_3d(base + SB_V + stage * SB_PANEL, &ba.mv, p0, h, r0 + vc * SB_L,
-                      bar(BAR_VFULL + stage));
-          ++vc;
+        if (may(qc, BAR_QFREE)) {
+          const uint32_t stage = qc & 1;
+          mbar_expect(bar(BAR_QFULL + stage), npanels * SB_PANEL);
+          for (int pl = 0; pl < npanels; ++pl)
+            tma_load_3d(base + SB_Q + (2 * stage + pl) * SB_PANEL, &ba.mq, 64 * pl, g,
+                        r0 + qc * SB_L, bar(BAR_QFULL + stage));
+          ++qc;
           moved = true;
         }
         if (moved) {
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           record_status(STATUS_TIMEOUT);
           break;
         }
-        __nanosleep(40);
+        __nanosleep(100);
       }
       if (*abort) {
         // loads in flight land before the block's memory is given up (each wait limited)
@@ -731,7 +734,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
     }
   } else {
-    // ------------------------------------------------ step sizes and decay sums
+    // ------------------------------------------------ step sizes and decay sums; product Y2
     const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
     const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
     float raw[4];
