@@ -6,11 +6,9 @@
 //   M'  = exp(c_L) M + sum_s exp(c_L - c_s) d_s k_s (x) v_s
 // so a block is four matrix products, all on tcgen05 with fp32 sums in tensor memory:
 //   S  = q k^T                      128 x 128 x N
-//   Y2 = q M                        128 x (2 x 64) x N, M as two bf16 parts (16 bits of it)
+//   Y2 = q M                        2 products 128 x 64 x N, M as two bf16 parts (16 bits of it)
 //   Y1 = (S o weights) v            128 x 64 x 128, weights rounded to bf16
 //   dM = k^T (w o v)                3 products N x 64 x 128, w o v as three bf16 parts (24 bits)
-// The parts of M lie side by side as columns of one product, so that q is read from shared
-// memory once for both.
 // The state is kept in fp32 registers and never rounded to less: dM has to be exact to fp32,
 // hence the three parts.  What enters y may be rounded to the type of y once: each token's
 // weight in another's read (half a step of bf16); two parts of M keep the second term below
@@ -22,8 +20,8 @@
 //   Y   a thread per token row: y = exp(c_t) Y2 + Y1 + D v, gated and stored
 //   H   a thread per state row: adds dM to the decayed state, publishes the state's two parts
 //   W   a thread per quarter row of v: w o v in parts, 32 tokens at a time
-//   and four single warps: step sizes and decay sums two blocks ahead, with Y2; dM; S and Y1;
-//   TMA loads
+//   and four single warps: step sizes and decay sums two blocks ahead; dM and Y1; Y2 and S;
+//   TMA loads of q and k (group Y loads v)
 // joined by mbarriers.  A block's work is a chain of short dependent steps; with the steps on
 // warps of their own the chains of successive blocks overlap.
 //
@@ -62,9 +60,9 @@ struct SsmPrep {
 constexpr uint32_t SB_BARS = SB_PREP + 2 * sizeof(SsmPrep);
 enum {
   BAR_QFULL = 0, BAR_QFREE = 2, BAR_KFULL = 4, BAR_KFREE = 6, BAR_VFULL = 8, BAR_VFREE = 10,
-  BAR_PREP = 12, BAR_PREPFREE = 14, BAR_WREADY = 16, BAR_WFREE = 18, BAR_CLEAN = 20,
-  BAR_S = 22, BAR_P = 24, BAR_Y = 26, BAR_DM = 28, BAR_DMFREE = 30, BAR_YFREE = 32, BAR_Y2,
-  BAR_Y2FREE, BAR_HREADY, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 3
+  BAR_PREP = 12, BAR_PREPFREE = 14, BAR_WREADY = 16, BAR_WFREE = 18, BAR_YFREE = 20,
+  BAR_S = 22, BAR_P = 24, BAR_Y = 26, BAR_DM = 28, BAR_DMFREE = 30, BAR_Y2 = 32,
+  BAR_HREADY = 34, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 2
 };
 constexpr uint32_t SB_TMEM_PTR = SB_BARS + 40 * 8;
 static_assert(BAR_COUNT <= 40, "barriers");
@@ -72,7 +70,7 @@ constexpr uint32_t SB_SMEM = SB_TMEM_PTR + 32 + 1024;      // and room to align
 static_assert(SB_SMEM <= 232448 - 64, "shared memory of a block");
 
 // Tensor memory columns: two buffers of S, whose first half becomes P and whose second half,
-// once weighed, holds Y1; Y2's two parts; two buffers of dM.
+// once weighed, holds Y1; two buffers each of Y2 and dM.
 constexpr uint32_t TM_S = 0, TM_Y1 = 64, TM_Y2 = 256, TM_DM = 384;
 
 constexpr float SB_LOG2E = 1.4426950408889634f;
@@ -245,28 +243,26 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(BAR_QFULL + i), 1);
-      mbar_init(bar(BAR_QFREE + i), 2);
+      mbar_init(bar(BAR_QFREE + i), 1);
       mbar_init(bar(BAR_KFULL + i), 1);
       mbar_init(bar(BAR_KFREE + i), 2);
       mbar_init(bar(BAR_VFULL + i), 1);
-      mbar_init(bar(BAR_VFREE + i), 5);
+      mbar_init(bar(BAR_VFREE + i), 4);
       mbar_init(bar(BAR_PREP + i), 1);
       mbar_init(bar(BAR_PREPFREE + i), 16);
       mbar_init(bar(BAR_WREADY + i), 4);
       mbar_init(bar(BAR_WFREE + i), 1);
-      mbar_init(bar(BAR_CLEAN + i), 4);
       mbar_init(bar(BAR_S + i), 1);
       mbar_init(bar(BAR_P + i), 4);
       mbar_init(bar(BAR_Y + i), 1);
+      mbar_init(bar(BAR_Y2 + i), 1);
+      mbar_init(bar(BAR_YFREE + i), 4);
       mbar_init(bar(BAR_DM + i), 1);
       mbar_init(bar(BAR_DMFREE + i), 4);
     }
-    mbar_init(bar(BAR_YFREE), 4);
-    mbar_init(bar(BAR_Y2), 1);
-    mbar_init(bar(BAR_Y2FREE), 4);
     mbar_init(bar(BAR_HREADY), 4);
     mbar_init(bar(BAR_HFREE), 1);
-    for (int i = 0; i < 3; ++i) mbar_init(bar(BAR_DRAIN + i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(BAR_DRAIN + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (npanels == 1) {  // state rows 64 and up: k is 0 there
@@ -378,6 +374,17 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const __nv_bfloat16* const zp =
         a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)h * a.P + p0 : nullptr;
     // whole sectors where rows start on them and hold a multiple of 16 values
+    // the group that reads a tile of v last also loads the next one into its place
+    auto load_v = [&](int c) {
+      mbar_expect(bar(BAR_VFULL + (c & 1)), SB_PANEL);
+      tma_load_3d(base + SB_V + (c & 1) * SB_PANEL, &ba.mv, p0, h, (int)(row0 + (long long)c * SB_L),
+                  bar(BAR_VFULL + (c & 1)));
+    };
+    int loaded = nb < 2 ? nb : 2;
+    if (warp == 4 && lane == 0) {
+      load_v(0);
+      if (nb > 1) load_v(1);
+    }
     const bool sectors = a.P % 16 == 0 && a.gate_stride % 16 == 0 &&
                          ((reinterpret_cast<uintptr_t>(yp) | reinterpret_cast<uintptr_t>(zp)) & 31) == 0;
     for (int c = 0; c < nb; ++c) {
@@ -412,16 +419,15 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       };
       if (zp && row + 2 * SB_L < row1) prefetch_l2(zrow + 2 * SB_L * a.gate_stride);
       load_z(0);  // on its way while the products finish
-      if (!wait(BAR_Y2, c) || !wait(BAR_Y + stage, c >> 1)) break;
+      if (!wait(BAR_Y2 + stage, c >> 1) || !wait(BAR_Y + stage, c >> 1)) break;
       tc_fence_after();
       const uint8_t* vtile = sm + SB_V + stage * SB_PANEL;
-      const uint32_t ybuf = tm + TM_S + stage * 128 + TM_Y1 + lanes, y2buf = tm + TM_Y2 + lanes;
+      const uint32_t ybuf = tm + TM_S + stage * 128 + TM_Y1 + lanes, y2buf = tm + TM_Y2 + stage * 64 + lanes;
 #pragma unroll 1
       for (int part = 0; part < 4; ++part) {
-        float y1[16], y2[16], y3[16];
+        float y1[16], y2[16];
         tmem_ld16(ybuf + 16 * part, y1);
         tmem_ld16(y2buf + 16 * part, y2);
-        tmem_ld16(y2buf + 64 + 16 * part, y3);
         const uint4 va = *reinterpret_cast<const uint4*>(vtile + tile_offset(t, 2 * part)),
                     vb = *reinterpret_cast<const uint4*>(vtile + tile_offset(t, 2 * part + 1));
         const uint32_t vw[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
@@ -429,10 +435,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 r = add2(make_float2(y2[2 * j], y2[2 * j + 1]),
-                                make_float2(y3[2 * j], y3[2 * j + 1]));
           o[j] = fma2(D2, unpack_bf16(vw[j]),
-                      fma2(f2, r, make_float2(y1[2 * j], y1[2 * j + 1])));
+                      fma2(f2, make_float2(y2[2 * j], y2[2 * j + 1]),
+                           make_float2(y1[2 * j], y1[2 * j + 1])));
         }
         if (zp) {
 #pragma unroll
@@ -459,11 +464,21 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(BAR_YFREE));
-        mbar_arrive(bar(BAR_Y2FREE));
+        mbar_arrive(bar(BAR_YFREE + stage));
         mbar_arrive(bar(BAR_VFREE + stage));
+        if (warp == 4 && c + 2 < nb && wait(BAR_VFREE + stage, c >> 1)) {
+          load_v(c + 2);
+          loaded = c + 3;
+          // a load from memory takes longer than a block's work: the one after that into L2
+          if (c + 4 < nb)
+            tma_prefetch_3d(&ba.mv, p0, h, (int)(row0 + (long long)(c + 4) * SB_L));
+        }
       }
+      __syncwarp();
     }
+    if (*abort && warp == 4 && lane == 0)
+      for (int c = loaded > 2 ? loaded - 2 : 0; c < loaded; ++c)
+        mbar_wait(bar(BAR_VFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
   } else if (warp < 12) {
     // ------------------------------------------------ H: row n = tid - 256
     const int n = tid - 256;
@@ -586,22 +601,40 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (lane == 0) mbar_arrive(bar(BAR_WREADY + buf));
       }
       if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive(bar(BAR_CLEAN + stage));
-        mbar_arrive(bar(BAR_PREPFREE + stage));
-      }
+      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + stage));
     }
   } else if (warp >= 16) {
   if (warp == 18) {
-    // ------------------------------------------------ products S and Y1
-    constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY1 = mma_desc(128, 64, 0, 1);
+    // ------------------------------------------------ products Y2 of a block and S of the next
+    constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY2 = mma_desc(128, 64, 0, 1);
     const uint32_t q0 = tile_desc(base + SB_Q), k0 = tile_desc(base + SB_K),
-                   v0 = tile_desc(base + SB_V);
-    for (int c = 0; c <= nb; ++c) {
-      if (c < nb) {
+                   h0 = tile_desc(base + SB_H);
+    for (int c = -1; c < nb; ++c) {
+      if (c >= 0) {
         const uint32_t stage = c & 1;
-        if (!wait(BAR_QFULL + stage, c >> 1) || !wait(BAR_KFULL + stage, c >> 1) ||
-            (c >= 2 && !wait(BAR_YFREE, c - 2)))
+        // the block's buffer of Y2 is free since its S was issued: group Y reads both
+        if (!wait(BAR_HREADY, c)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t q = q0 + stage * (2 * SB_PANEL >> 4);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t o = ((i >> 2 & 1) * SB_PANEL + (i & 3) * 32) >> 4;
+            if ((i & 7) < nk)
+              mma_ss(tm + TM_Y2 + stage * 64, q + o,
+                     h0 + (((i >> 3) * SB_PANEL + (i & 7) * 2048) >> 4), dY2, i > 0);
+          }
+          mma_commit(bar(BAR_Y2 + stage));
+          mma_commit(bar(BAR_HFREE));
+          mma_commit(bar(BAR_QFREE + stage));
+        }
+        __syncwarp();
+      }
+      const int e = c + 1;
+      if (e < nb) {
+        const uint32_t stage = e & 1;
+        if (!wait(BAR_QFULL + stage, e >> 1) || !wait(BAR_KFULL + stage, e >> 1) ||
+            (e >= 2 && !wait(BAR_YFREE + stage, (e >> 1) - 1)))
           break;
         tc_fence_after();
         if (elect_one()) {
@@ -613,24 +646,6 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           }
           mma_commit(bar(BAR_S + stage));
           mma_commit(bar(BAR_KFREE + stage));
-          mma_commit(bar(BAR_QFREE + stage));
-        }
-        __syncwarp();
-      }
-      if (c > 0) {
-        const int e = c - 1;
-        const uint32_t stage = e & 1;
-        if (!wait(BAR_CLEAN + stage, e >> 1) || !wait(BAR_VFULL + stage, e >> 1) ||
-            !wait(BAR_P + stage, e >> 1))
-          break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t v = v0 + stage * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
-#pragma unroll
-          for (int i = 0; i < SB_L / 16; ++i)
-            mma_ts(s + TM_Y1, s + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
-          mma_commit(bar(BAR_Y + stage));
-          mma_commit(bar(BAR_VFREE + stage));
         }
         __syncwarp();
       }
@@ -639,9 +654,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     __syncwarp();
     mbar_wait(bar(BAR_DRAIN), 0, abort);
   } else if (warp == 17) {
-    // ------------------------------------------------ product dM, the parts onto one another
-    constexpr uint32_t dM = mma_desc(128, 64, 1, 1);
-    const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W);
+    // ------------------------------------------------ products dM, part onto part, and Y1
+    constexpr uint32_t dM = mma_desc(128, 64, 1, 1), dY1 = mma_desc(128, 64, 0, 1);
+    const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W),
+                   v0 = tile_desc(base + SB_V);
     bool ok = true;
     for (int c = 0; c < nb && ok; ++c) {
       const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
@@ -666,75 +682,52 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         }
         __syncwarp();
       }
+      // the last quarter is also the sign that v's rows behind the end are zeros
+      ok = ok && wait(BAR_VFULL + stage, c >> 1) && wait(BAR_P + stage, c >> 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t v = v0 + stage * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
+#pragma unroll
+        for (int i = 0; i < SB_L / 16; ++i)
+          mma_ts(s + TM_Y1, s + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
+        mma_commit(bar(BAR_Y + stage));
+      }
+      __syncwarp();
     }
     if (elect_one()) mma_commit(bar(BAR_DRAIN + 1));
     __syncwarp();
     mbar_wait(bar(BAR_DRAIN + 1), 0, abort);
   } else if (warp == 19) {
-    // ------------------------------------------------ loads: each tile as soon as its place is free
+    // ------------------------------------------------ loads of k and q
     if (lane == 0) {
-      int kc = 0, vc = 0, qc = 0;  // blocks whose load is issued
-      const int r0 = (int)row0;
-      unsigned long long since = 0;
-      auto may = [&](int c, int free_bar) {
-        return c < nb &&
-               (c < 2 || mbar_test(bar(free_bar + (c & 1)), (uint32_t)((c >> 1) - 1) & 1u));
-      };
-      while (kc < nb || vc < nb || qc < nb) {
-        bool moved = false;
-        if (may(vc, BAR_VFREE)) {
-          const uint32_t stage = vc & 1;
-          mbar_expect(bar(BAR_VFULL + stage), SB_PANEL);
-          tma_load_3d(base + SB_V + stage * SB_PANEL, &ba.mv, p0, h, r0 + vc * SB_L,
-                      bar(BAR_VFULL + stage));
-          // two blocks ahead into L2: a load from memory takes longer than a block's work
-          if (vc + 2 < nb) tma_prefetch_3d(&ba.mv, p0, h, r0 + (vc + 2) * SB_L);
-          ++vc;
-          moved = true;
-        }
-        if (may(kc, BAR_KFREE)) {
-          const uint32_t stage = kc & 1;
-          mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
-          for (int pl = 0; pl < npanels; ++pl)
-            tma_load_3d(base + SB_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g,
-                        r0 + kc * SB_L, bar(BAR_KFULL + stage));
-          ++kc;
-          moved = true;
-        }
-        if (may(qc, BAR_QFREE)) {
-          const uint32_t stage = qc & 1;
-          mbar_expect(bar(BAR_QFULL + stage), npanels * SB_PANEL);
-          for (int pl = 0; pl < npanels; ++pl)
-            tma_load_3d(base + SB_Q + (2 * stage + pl) * SB_PANEL, &ba.mq, 64 * pl, g,
-                        r0 + qc * SB_L, bar(BAR_QFULL + stage));
-          ++qc;
-          moved = true;
-        }
-        if (moved) {
-          since = 0;
-          continue;
-        }
-        if (*abort) break;
-        const unsigned long long now = wall_ns();
-        if (since == 0) since = now;
-        if (now - since > MBAR_LIMIT_NS) {
-          *abort = 1;
-          record_status(STATUS_TIMEOUT);
-          break;
-        }
-        __nanosleep(100);
+      int kc = 0, qc = 0;  // blocks whose load is issued
+      for (int c = 0; c < nb; ++c) {
+        const uint32_t stage = c & 1;
+        const int r = (int)(row0 + (long long)c * SB_L);
+        if (c >= 2 && !wait(BAR_QFREE + stage, (c >> 1) - 1)) break;
+        mbar_expect(bar(BAR_QFULL + stage), npanels * SB_PANEL);
+        for (int pl = 0; pl < npanels; ++pl)
+          tma_load_3d(base + SB_Q + (2 * stage + pl) * SB_PANEL, &ba.mq, 64 * pl, g, r,
+                      bar(BAR_QFULL + stage));
+        qc = c + 1;
+        if (c >= 2 && !wait(BAR_KFREE + stage, (c >> 1) - 1)) break;
+        mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
+        for (int pl = 0; pl < npanels; ++pl)
+          tma_load_3d(base + SB_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
+                      bar(BAR_KFULL + stage));
+        kc = c + 1;
       }
       if (*abort) {
         // loads in flight land before the block's memory is given up (each wait limited)
-        int none = 0;
-        const int n[3] = {qc, kc, vc}, full[3] = {BAR_QFULL, BAR_KFULL, BAR_VFULL};
-        for (int i = 0; i < 3; ++i)
-          for (int c = n[i] > 2 ? n[i] - 2 : 0; c < n[i]; ++c)
-            mbar_wait(bar(full[i] + (c & 1)), (uint32_t)(c >> 1) & 1u, &none);
+        for (int c = qc > 2 ? qc - 2 : 0; c < qc; ++c)
+          mbar_wait(bar(BAR_QFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
+        for (int c = kc > 2 ? kc - 2 : 0; c < kc; ++c)
+          mbar_wait(bar(BAR_KFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
       }
     }
   } else {
-    // ------------------------------------------------ step sizes and decay sums; product Y2
+    // ------------------------------------------------ step sizes and decay sums
     const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
     const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
     float raw[4];
@@ -770,32 +763,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       if (lane == 0) mbar_arrive(bar(BAR_PREP + (c & 1)));
       return true;
     };
-    constexpr uint32_t dY2 = mma_desc(128, 128, 0, 1);
-    const uint32_t q0 = tile_desc(base + SB_Q), h0 = tile_desc(base + SB_H, SB_PANEL);
-    bool ok = prepare(0) && (nb < 2 || prepare(1));
-    for (int c = 0; c < nb && ok; ++c) {
-      const uint32_t stage = c & 1;
-      ok = wait(BAR_HREADY, c) && wait(BAR_QFULL + stage, c >> 1) &&
-           (c == 0 || wait(BAR_Y2FREE, c - 1));
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t q = q0 + stage * (2 * SB_PANEL >> 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t o = ((i >> 2) * SB_PANEL + (i & 3) * 32) >> 4;
-          if (i < nk) mma_ss(tm + TM_Y2, q + o, h0 + i * (2048 >> 4), dY2, i > 0);
-        }
-        mma_commit(bar(BAR_Y2));
-        mma_commit(bar(BAR_HFREE));
-        mma_commit(bar(BAR_QFREE + stage));
-      }
-      __syncwarp();
-      if (c + 2 < nb) ok = prepare(c + 2);
-    }
-    if (elect_one()) mma_commit(bar(BAR_DRAIN + 2));
-    __syncwarp();
-    mbar_wait(bar(BAR_DRAIN + 2), 0, abort);
+    for (int c = 0; c < nb; ++c)
+      if (!prepare(c)) break;
   }
   }
   tc_fence_before();
