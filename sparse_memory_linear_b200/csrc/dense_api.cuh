@@ -166,15 +166,6 @@ bool ssm_pointers(const sdm_ssm_shape& s, long long R, const void* k, const void
   return true;
 }
 
-template <typename T>
-cudaError_t launch_ssm_scan(const SsmArgs& a, dim3 grid, cudaStream_t st) {
-  const dim3 block(128);
-  if (a.N <= 32) return launch_pdl<true>(ssm_scan_kernel<T, 1>, grid, block, 0, st, a);
-  if (a.N <= 64) return launch_pdl<true>(ssm_scan_kernel<T, 2>, grid, block, 0, st, a);
-  if (a.N <= 128) return launch_pdl<true>(ssm_scan_kernel<T, 4>, grid, block, 0, st, a);
-  return launch_pdl<true>(ssm_scan_kernel<T, 8>, grid, block, 0, st, a);
-}
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -217,31 +208,35 @@ bool ssm_block_fits(const sdm_ssm_shape& s, long long R) {
   return s.in_dtype == SDM_BF16 && s.N <= 128 && s.T >= 16 && R < 2147483647LL;
 }
 
-// How the block-wise scan cuts sequences into segments.  A CTA walks one segment of one (head, 64
-// columns) tile at one block of 128 tokens in about SSM_WALK_US; a pass that makes the segments'
-// own contributions costs SSM_PRE_US a block, and with the chain over segments SSM_SPLIT_US at
-// least.  The number of segments is the one with the least estimated time; packed batches,
-// whose lengths only the device knows, are cut as one sequence of all rows would be.
-constexpr double SSM_WALK_US = 3.0, SSM_PRE_US = 0.7, SSM_SPLIT_US = 12.0;
+// How a scan cuts sequences into segments.  A CTA walks a segment `unit` rows at a time in about
+// walk_us, `slots` CTAs at once; the pass that makes the segments' own contributions costs pre_us
+// a unit, and with the chain over segments split_us at least.  The number of segments is the one
+// with the least estimated time; packed batches, whose lengths only the device knows, are cut
+// as one sequence of all rows would be.
+struct SsmCost {
+  int unit, slots;
+  double walk_us, pre_us, split_us;
+};
 
 struct SsmPlan {
-  long long seg_blocks, items;  // blocks of a segment; (sequence, segment) pairs at most
+  long long seg_rows, items;  // rows of a segment; (sequence, segment) pairs at most
   bool split;
   size_t off_decays, bytes;
 };
 
-SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms) {
-  const long long L = ((long long)s.T + SB_L - 1) / SB_L, units = (long long)s.H *
-                  ((s.d_v + SB_P - 1) / SB_P), seqs = packed ? 1 : s.B;
-  auto waves = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
+SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, const SsmCost& c) {
+  const long long L = ((long long)s.T + c.unit - 1) / c.unit, seqs = packed ? 1 : s.B;
+  auto waves = [&](long long items) {
+    return (double)((items * ctas_per_item + c.slots - 1) / c.slots);
+  };
   long long best = 1;
-  double least = waves(seqs * units) * L * SSM_WALK_US;
-  const long long most = 6LL * sms / (seqs * units) + 1;  // more waves gain nothing
+  double least = waves(seqs) * L * c.walk_us;
+  const long long most = 6LL * c.slots / (seqs * ctas_per_item) + 1;  // more waves gain nothing
   for (long long n = 2; n <= L && n <= most; ++n) {
-    const long long len = (L + n - 1) / n, segs = (L + len - 1) / len;
-    if (segs != n) continue;
-    const double t = waves(seqs * n * units) * len * SSM_WALK_US +
-                     waves(seqs * (n - 1) * units) * len * SSM_PRE_US + SSM_SPLIT_US;
+    const long long len = (L + n - 1) / n;
+    if ((L + len - 1) / len != n) continue;
+    const double t = waves(seqs * n) * len * c.walk_us + waves(seqs * (n - 1)) * len * c.pre_us +
+                     c.split_us;
     if (t < least) {
       least = t;
       best = n;
@@ -249,9 +244,9 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms) {
   }
   SsmPlan p = {};
   p.split = best > 1;
-  p.seg_blocks = L > 0 ? (L + best - 1) / best : 1;
-  const long long seg_rows = p.seg_blocks * SB_L;
-  p.items = packed ? s.T / seg_rows + s.B : s.B * (s.T > 0 ? (s.T + seg_rows - 1) / seg_rows : 1);
+  p.seg_rows = (L > 0 ? (L + best - 1) / best : 1) * c.unit;
+  p.items = packed ? s.T / p.seg_rows + s.B
+                   : s.B * (s.T > 0 ? (s.T + p.seg_rows - 1) / p.seg_rows : 1);
   if (p.split) {
     p.off_decays = round_up((size_t)p.items * s.H * s.N * s.d_v * 4, WS_ALIGN);
     p.bytes = p.off_decays + round_up((size_t)p.items * s.H * 4, WS_ALIGN);
@@ -259,15 +254,64 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms) {
   return p;
 }
 
+SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
+  if (block)
+    return ssm_plan(s, packed, (long long)s.H * ((s.d_v + SB_P - 1) / SB_P),
+                    SsmCost{SB_L, sms, 3.5, 1.9, 12.0});
+  return ssm_plan(s, packed, (long long)s.H * ((s.d_v + SSM_COLS - 1) / SSM_COLS),
+                  SsmCost{16, 5 * sms, 1.6, 1.2, 12.0});
+}
+
+SsmSplit ssm_split(const SsmPlan& plan, void* ws) {
+  return SsmSplit{plan.seg_rows, static_cast<float*>(ws),
+                  reinterpret_cast<float*>(static_cast<char*>(ws) + plan.off_decays)};
+}
+
+cudaError_t launch_ssm_chain(const sdm_ssm_shape& s, const SsmArgs& a, const SsmSplit& sp,
+                             cudaStream_t st) {
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return launch_pdl<true>(ssm_chain_kernel,
+                          dim3((unsigned)s.B, (unsigned)s.H,
+                               (unsigned)((s.N * s.d_v / 4 + 255) / 256)),
+                          dim3(256), 0, st, a, sp);
+}
+
+template <typename T, bool CONTRIB>
+cudaError_t launch_ssm_scan(const SsmArgs& a, const SsmSplit& sp, dim3 grid, cudaStream_t st) {
+  const dim3 block(128);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  if (a.N <= 32)
+    return launch_pdl<true>(ssm_scan_kernel<T, 1, CONTRIB>, grid, block, 0, st, a, sp);
+  if (a.N <= 64)
+    return launch_pdl<true>(ssm_scan_kernel<T, 2, CONTRIB>, grid, block, 0, st, a, sp);
+  if (a.N <= 128)
+    return launch_pdl<true>(ssm_scan_kernel<T, 4, CONTRIB>, grid, block, 0, st, a, sp);
+  return launch_pdl<true>(ssm_scan_kernel<T, 8, CONTRIB>, grid, block, 0, st, a, sp);
+}
+
+template <typename T>
+sdm_status ssm_scan_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceInfo* di, void* ws,
+                        cudaStream_t st) {
+  const SsmPlan plan = ssm_plan(s, a.seq.cu != nullptr, di->sms, false);
+  if (plan.items > 2147483647LL) return SDM_ERR_UNSUPPORTED;
+  const SsmSplit sp = ssm_split(plan, ws);
+  const dim3 grid((unsigned)plan.items, (unsigned)s.H,
+                  (unsigned)((s.d_v + SSM_COLS - 1) / SSM_COLS));
+  if (plan.split) {
+    SDM_CUDA_TRY((launch_ssm_scan<T, true>(a, sp, grid, st)));
+    SDM_CUDA_TRY(launch_ssm_chain(s, a, sp, st));
+  }
+  SDM_CUDA_TRY((launch_ssm_scan<T, false>(a, sp, grid, st)));
+  return SDM_OK;
+}
+
 sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceInfo* di, void* ws,
                          cudaStream_t st) {
-  const SsmPlan plan = ssm_plan(s, a.seq.cu != nullptr, di->sms);
+  const SsmPlan plan = ssm_plan(s, a.seq.cu != nullptr, di->sms, true);
   SsmBlockArgs ba;
   ba.a = a;
-  ba.seg_blocks = (int)plan.seg_blocks;
+  ba.sp = ssm_split(plan, ws);
   ba.ptiles = (s.d_v + SB_P - 1) / SB_P;
-  ba.starts = static_cast<float*>(ws);
-  ba.decays = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.off_decays);
   if (!tile_map(&ba.mq, a.q, s.N, s.G, a.seq.R, a.q_stride) ||
       !tile_map(&ba.mk, a.k, s.N, s.G, a.seq.R, a.k_stride) ||
       !tile_map(&ba.mv, a.v, s.d_v, s.H, a.seq.R, a.v_stride))
@@ -277,11 +321,8 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
   if (plan.split) {
     SDM_CUDA_TRY(launch_pdl(ssm_segment_kernel, dim3((unsigned)blocks), dim3(SG_THREADS),
                             (size_t)SG_SMEM, st, ba));
-    SDM_CUDA_TRY(launch_pdl(ssm_chain_kernel,
-                            dim3((unsigned)s.B, (unsigned)s.H,
-                                 (unsigned)((s.N * s.d_v / 4 + 255) / 256)),
-                            dim3(256), 0, st, ba));
-    g_launches.fetch_add(2, std::memory_order_relaxed);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    SDM_CUDA_TRY(launch_ssm_chain(s, a, ba.sp, st));
   }
   SDM_CUDA_TRY(launch_pdl(ssm_block_kernel, dim3((unsigned)blocks), dim3(SB_THREADS),
                           (size_t)SB_SMEM, st, ba));
@@ -330,11 +371,10 @@ size_t sdm_ssm_workspace_size(sdm_ssm_shape shape) {
   DeviceInfo* di;
   if (!ssm_args(shape, false, &a)) return 0;
   size_t need = WS_ALIGN;
-  if (!ssm_block_fits(shape, 0)) return need;
   // without a device (sizes asked for ahead of time) a B200's number of multiprocessors
   const int sms = device_info(&di) == SDM_OK ? di->sms : 148;
   for (const bool packed : {false, true}) {
-    const size_t n = ssm_plan(shape, packed, sms).bytes;
+    const size_t n = ssm_plan(shape, packed, sms, ssm_block_fits(shape, 0)).bytes;
     if (n > need) need = n;
   }
   return need;
@@ -369,13 +409,8 @@ sdm_status sdm_ssm_forward(const void* k, const void* q, const void* v, const vo
   a.from_zero = init == SDM_INIT_ZERO;
   ProfScope ps(SDM_KERNEL_SSM, st);
   if (ssm_block_fits(s, R)) return ssm_block_run(s, a, di, ws, st);
-  const dim3 grid((unsigned)s.B, (unsigned)s.H, (unsigned)((s.d_v + SSM_COLS - 1) / SSM_COLS));
-  if (s.in_dtype == SDM_BF16)
-    SDM_CUDA_TRY(launch_ssm_scan<__nv_bfloat16>(a, grid, st));
-  else
-    SDM_CUDA_TRY(launch_ssm_scan<float>(a, grid, st));
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  return SDM_OK;
+  return s.in_dtype == SDM_BF16 ? ssm_scan_run<__nv_bfloat16>(s, a, di, ws, st)
+                                : ssm_scan_run<float>(s, a, di, ws, st);
 }
 
 sdm_status sdm_ssm_step(const void* k, const void* q, const void* v, const void* dt,

@@ -48,27 +48,114 @@ __device__ __forceinline__ float ssm_step_size(float dt, int softplus) {
   return dt < 0.0f ? 0.0f : dt;
 }
 
+// The (sequence, segment) of work item `item`: a sequence of n rows has max(1, ceil(n / seg))
+// segments.  Called by one warp; false past the last.
+__device__ __forceinline__ bool ssm_find_item(const SeqBounds& seq, long long item, long long seg,
+                                              int* b_out, long long* s_out) {
+  if (!seq.cu) {
+    const long long per = seq.T > 0 ? (seq.T + seg - 1) / seg : 1;
+    *b_out = (int)(item / per);
+    *s_out = item % per;
+    return *b_out < seq.B;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < seq.B; b0 += 32) {
+    const int b = b0 + lane;
+    long long n = 0;
+    if (b < seq.B) {
+      const long long len = seq.end(b) - seq.start(b);
+      n = len > 0 ? (len + seg - 1) / seg : 1;
+    }
+    long long upto = n;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const long long o = __shfl_up_sync(FULL_MASK, upto, s);
+      if (lane >= s) upto += o;
+    }
+    const unsigned hit = __ballot_sync(FULL_MASK, upto > item);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      *b_out = b0 + l;
+      *s_out = item - __shfl_sync(FULL_MASK, upto - n, l);
+      return true;
+    }
+    item -= __shfl_sync(FULL_MASK, upto, 31);
+  }
+  return false;
+}
+
+// Sequences cut into segments that are scanned at the same time (where there are few CTAs): a
+// first pass makes each segment's own contribution from a zero state, a chain over the
+// segments turns those into the states before them, and the scan starts from these.
+struct SsmSplit {
+  long long seg_rows;  // rows of a segment
+  float* starts;       // [items, H, N, P]: the state before each segment of a split sequence
+  float* decays;       // [items, H]: the segment's whole decay
+};
+
 // Token-by-token scan.  A block holds 16 of a head's d_v columns: four per warp, eight lanes to
-// a column, each lane with the state rows 32 j + 4 l .. + 3 in registers.  Tokens come through
-// shared memory 16 at a time.  The chain from token to token is one multiply-add per state
-// value; the sum over the rows ends in three shuffles.
-constexpr int SSM_TB = 16;    // tokens staged at a time
+// a column, each lane with the state rows 32 j + 4 l .. + 3 in registers.  The chain from token
+// to token is one multiply-add per state value; the sum over the rows ends in three shuffles.
+// Tokens come through shared memory a tile at a time, the tile after next already on its way
+// (cp.async): with a tile loaded only when the one before was done, the loads' latency was
+// nine tenths of the time.  CONTRIB: the first pass of a split (no reads, no y).
 constexpr int SSM_COLS = 16;  // columns of a block
 
-template <typename T, int NJ>
-__global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a) {
+template <typename T>
+__device__ __forceinline__ float4 load4_f32(const T* p);
+template <>
+__device__ __forceinline__ float4 load4_f32<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4_f32<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+template <typename T, int NJ, bool CONTRIB>
+__global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
   grid_dependency_wait();
   grid_launch_dependents();
-  constexpr int NP = 32 * NJ;
-  __shared__ __align__(16) float sk[SSM_TB][NP];
-  __shared__ __align__(16) float sq[SSM_TB][NP];
-  __shared__ float sv[SSM_TB][SSM_COLS], sy[SSM_TB][SSM_COLS];
-  __shared__ float sd[SSM_TB], sa[SSM_TB];
+  constexpr int NP = 32 * NJ, TB = NJ >= 8 ? 8 : 16, E = 16 / sizeof(T);
+  constexpr int VC = SSM_COLS / E;  // 16-byte pieces of a row of the block's columns
+  __shared__ __align__(16) T sk[2][TB][NP], sq[CONTRIB ? 1 : 2][CONTRIB ? 1 : TB][NP];
+  __shared__ __align__(16) T sv[2][TB][SSM_COLS], sz[2][TB][SSM_COLS];
+  __shared__ float sy[2][TB][SSM_COLS], sd[2][TB], sa[2][TB];
+  __shared__ int s_ok, s_b;
+  __shared__ long long s_seg;
   const int tid = threadIdx.x, lane = tid & 31, ln = lane & 7;
   const int col = (tid >> 5) * 4 + (lane >> 3);
   const int h = blockIdx.y, g = h / (a.H / a.G);
   const int p0 = blockIdx.z * SSM_COLS, p = p0 + col;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.seq.check();
+  if (!CONTRIB && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.seq.check();
+  if (tid < 32) {
+    int b = 0;
+    long long seg = 0;
+    const bool ok = ssm_find_item(a.seq, blockIdx.x, sp.seg_rows, &b, &seg);
+    if (tid == 0) {
+      s_ok = ok;
+      s_b = b;
+      s_seg = seg;
+    }
+  }
+  // columns of rows that do not exist stay 0
+  for (int i = tid; i < 2 * TB * NP; i += 128) {
+    const int n = i % NP;
+    if (n >= a.N) {
+      (&sk[0][0][0])[i] = from_f32<T>(0.0f);
+      if (!CONTRIB) (&sq[0][0][0])[i] = from_f32<T>(0.0f);
+    }
+  }
+  for (int i = tid; i < 2 * TB * SSM_COLS; i += 128) (&sv[0][0][0])[i] = from_f32<T>(0.0f);
+  __syncthreads();
+  if (!s_ok) return;
+  const int b = s_b;
+  const long long seq0 = a.seq.start(b), seq1 = a.seq.end(b), r0 = seq0 + s_seg * sp.seg_rows;
+  const long long r1 = r0 + sp.seg_rows < seq1 ? r0 + sp.seg_rows : seq1;
+  const bool split = seq1 - seq0 > sp.seg_rows;
+  if (CONTRIB && r1 == seq1) return;  // nothing follows the last segment
   const T* kp = static_cast<const T*>(a.k) + (size_t)g * a.N;
   const T* qp = static_cast<const T*>(a.q) + (size_t)g * a.N;
   const T* vp = static_cast<const T*>(a.v) + (size_t)h * a.P + p0;
@@ -76,73 +163,173 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a) {
   const T* dp = static_cast<const T*>(a.dt) + h;
   T* yp = static_cast<T*>(a.y) + (size_t)h * a.P + p0;
   const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f, D = a.D ? a.D[h] : 0.0f;
-  for (int b = blockIdx.x; b < a.seq.B; b += gridDim.x) {
-    const long long s0 = a.seq.start(b), e0 = a.seq.end(b);
-    float* Mp = a.M + ((size_t)b * a.H + h) * a.N * a.P;
-    float s[NJ][4];
+  float* Mp = a.M + ((size_t)b * a.H + h) * a.N * a.P;
+  const float* from =
+      split ? sp.starts + ((size_t)blockIdx.x * a.H + h) * a.N * a.P : Mp;
+  float* to = CONTRIB ? sp.starts + ((size_t)(blockIdx.x + 1) * a.H + h) * a.N * a.P : Mp;
+  float s[NJ][4];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = 32 * j + 4 * ln + i;
-        s[j][i] = !a.from_zero && n < a.N && p < a.P ? Mp[(size_t)n * a.P + p] : 0.0f;
-      }
-    for (long long t0 = s0; t0 < e0; t0 += SSM_TB) {
-      const int nt = e0 - t0 < SSM_TB ? (int)(e0 - t0) : SSM_TB;
-      __syncthreads();
-      for (int i = tid; i < nt * NP; i += 128) {
-        const int t = i / NP, n = i % NP;
-        const bool in = n < a.N;
-        sk[t][n] = in ? to_f32(kp[(t0 + t) * a.k_stride + n]) : 0.0f;
-        sq[t][n] = in ? to_f32(qp[(t0 + t) * a.q_stride + n]) : 0.0f;
-      }
-      for (int i = tid; i < nt * SSM_COLS; i += 128) {
-        const int t = i / SSM_COLS, c = i % SSM_COLS;
-        sv[t][c] = p0 + c < a.P ? to_f32(vp[(t0 + t) * a.v_stride + c]) : 0.0f;
-      }
-      if (tid < nt) {
-        const float d = ssm_step_size(to_f32(dp[(t0 + tid) * a.dt_stride]) + bias, a.softplus);
-        sd[tid] = d;
-        sa[tid] = expf(d * A);
-      }
-      __syncthreads();
-#pragma unroll 2
-      for (int t = 0; t < nt; ++t) {
-        const float al = sa[t], dv = sd[t] * sv[t][col];
-        float acc = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const int n = 32 * j + 4 * ln + i;
+      s[j][i] = !CONTRIB && (split || !a.from_zero) && n < a.N && p < a.P
+                    ? from[(size_t)n * a.P + p]
+                    : 0.0f;
+    }
+  const int tiles = (int)((r1 - r0 + TB - 1) / TB);
+  auto rows_of = [&](int i) {
+    const long long left = r1 - (r0 + (long long)i * TB);
+    return left < TB ? (int)left : TB;
+  };
+  float raw = 0.0f;  // dt of the tile to come, a token to each of the first TB threads
+  auto load = [&](int i) {
+    const long long t0 = r0 + (long long)i * TB;
+    const int nt = rows_of(i), buf = i & 1, pieces = a.N / E;
+    for (int e = tid; e < nt * pieces; e += 128) {
+      const int t = e / pieces, c = (e - t * pieces) * E;
+      cp_async16(&sk[buf][t][c], kp + (t0 + t) * a.k_stride + c);
+      if (!CONTRIB) cp_async16(&sq[CONTRIB ? 0 : buf][CONTRIB ? 0 : t][c],
+                               qp + (t0 + t) * a.q_stride + c);
+    }
+    for (int e = tid; e < nt * VC; e += 128) {
+      const int t = e / VC, c = (e - t * VC) * E;
+      if (p0 + c >= a.P) continue;
+      cp_async16(&sv[buf][t][c], vp + (t0 + t) * a.v_stride + c);
+      if (!CONTRIB && zp) cp_async16(&sz[buf][t][c], zp + (t0 + t) * a.gate_stride + c);
+    }
+    cp_async_commit();
+  };
+  auto load_dt = [&](int i) {
+    if (tid < TB && tid < rows_of(i))
+      raw = to_f32(dp[(r0 + (long long)i * TB + tid) * a.dt_stride]);
+  };
+  float decay = 0.0f;  // the segment's summed d A (CONTRIB)
+  if (tiles > 0) {
+    load(0);
+    load_dt(0);
+  }
+  for (int i = 0; i < tiles; ++i) {
+    const int buf = i & 1, nt = rows_of(i);
+    if (tid < TB) {
+      // a tile's missing tokens are steps of size 0: they change nothing
+      const float d = tid < nt ? ssm_step_size(raw + bias, a.softplus) : 0.0f;
+      sd[buf][tid] = d;
+      sa[buf][tid] = expf(d * A);
+      if (CONTRIB) decay += d * A;
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    if (i + 1 < tiles) {
+      load(i + 1);
+      load_dt(i + 1);
+    }
+#pragma unroll 4
+    for (int t = 0; t < TB; ++t) {
+      const float al = sa[buf][t], dv = t < nt ? sd[buf][t] * to_f32(sv[buf][t][col]) : 0.0f;
+      float acc = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const float4 k4 = *reinterpret_cast<const float4*>(&sk[t][32 * j + 4 * ln]);
-          const float4 q4 = *reinterpret_cast<const float4*>(&sq[t][32 * j + 4 * ln]);
+      for (int j = 0; j < NJ; ++j) {
+        const float4 k4 = load4_f32(&sk[buf][t][32 * j + 4 * ln]);
+        // a missing token's k may be anything: it must not meet dv
+        if (t < nt) {
           s[j][0] = fmaf(s[j][0], al, dv * k4.x);
           s[j][1] = fmaf(s[j][1], al, dv * k4.y);
           s[j][2] = fmaf(s[j][2], al, dv * k4.z);
           s[j][3] = fmaf(s[j][3], al, dv * k4.w);
+        }
+        if (!CONTRIB) {
+          const float4 q4 = load4_f32(&sq[CONTRIB ? 0 : buf][CONTRIB ? 0 : t][32 * j + 4 * ln]);
           acc = fmaf(q4.x, s[j][0], acc);
           acc = fmaf(q4.y, s[j][1], acc);
           acc = fmaf(q4.z, s[j][2], acc);
           acc = fmaf(q4.w, s[j][3], acc);
         }
+      }
+      if (!CONTRIB) {
 #pragma unroll
         for (int m = 1; m < 8; m <<= 1) acc += __shfl_xor_sync(FULL_MASK, acc, m);
-        if (ln == 0) sy[t][col] = acc;
-      }
-      __syncthreads();
-      for (int i = tid; i < nt * SSM_COLS; i += 128) {
-        const int t = i / SSM_COLS, c = i % SSM_COLS;
-        if (p0 + c >= a.P) continue;
-        float y = sy[t][c];
-        if (a.D) y = fmaf(D, sv[t][c], y);
-        if (zp) y *= gate_act(to_f32(zp[(t0 + t) * a.gate_stride + c]), a.act);
-        yp[(size_t)(t0 + t) * a.H * a.P + c] = from_f32<T>(y);
+        if (ln == 0) sy[buf][t][col] = acc;
       }
     }
+    __syncthreads();
+    if (!CONTRIB) {
+      const long long t0 = r0 + (long long)i * TB;
+      for (int e = tid; e < nt * SSM_COLS; e += 128) {
+        const int t = e / SSM_COLS, c = e % SSM_COLS;
+        if (p0 + c >= a.P) continue;
+        float y = sy[buf][t][c];
+        if (a.D) y = fmaf(D, to_f32(sv[buf][t][c]), y);
+        if (zp) y *= gate_act(to_f32(sz[buf][t][c]), a.act);
+        yp[(size_t)(t0 + t) * a.H * a.P + c] = from_f32<T>(y);
+      }
+      __syncthreads();
+    }
+  }
+  if (CONTRIB || r1 == seq1) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = 32 * j + 4 * ln + i;
-        if (n < a.N && p < a.P) Mp[(size_t)n * a.P + p] = s[j][i];
+        if (n < a.N && p < a.P) to[(size_t)n * a.P + p] = s[j][i];
+      }
+  }
+  if (CONTRIB && p0 == 0 && tid < 32) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) decay += __shfl_xor_sync(FULL_MASK, decay, m);
+    if (tid == 0) sp.decays[(size_t)blockIdx.x * a.H + h] = expf(decay);
+  }
+}
+
+// The states before the segments of a split sequence, from the first on: what the sequence
+// starts with, then each segment's decay and contribution.  A block per (sequence, head, 1024
+// state values); eight segments' values are on their way at a time.
+__global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  __shared__ unsigned long long s_first;
+  const int b = blockIdx.x, h = blockIdx.y, i = blockIdx.z * 256 + threadIdx.x;
+  const long long seg = sp.seg_rows, len = a.seq.end(b) - a.seq.start(b);
+  if (len <= seg) return;
+  if (threadIdx.x == 0) s_first = a.seq.cu ? 0 : b * ((a.seq.T + seg - 1) / seg);
+  __syncthreads();
+  if (a.seq.cu) {
+    long long items = 0;
+    for (int e = threadIdx.x; e < b; e += 256) {
+      const long long n = a.seq.end(e) - a.seq.start(e);
+      items += n > 0 ? (n + seg - 1) / seg : 1;
+    }
+    if (items) atomicAdd(&s_first, (unsigned long long)items);
+  }
+  __syncthreads();
+  const int n4 = a.N * a.P / 4;
+  if (i >= n4) return;
+  const long long first = (long long)s_first;
+  const int segs = (int)((len + seg - 1) / seg);
+  const size_t step = (size_t)a.H * n4;
+  float4* at = reinterpret_cast<float4*>(sp.starts) + ((size_t)first * a.H + h) * n4 + i;
+  const float* decay = sp.decays + first * a.H + h;
+  float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!a.from_zero) m = reinterpret_cast<const float4*>(a.M)[((size_t)b * a.H + h) * n4 + i];
+  at[0] = m;
+  for (int s0 = 1; s0 < segs; s0 += 8) {
+    float4 e[8];
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (s0 + j < segs) {
+        e[j] = at[(s0 + j) * step];
+        f[j] = decay[(size_t)(s0 + j - 1) * a.H];
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (s0 + j < segs) {
+        m.x = fmaf(m.x, f[j], e[j].x);
+        m.y = fmaf(m.y, f[j], e[j].y);
+        m.z = fmaf(m.z, f[j], e[j].z);
+        m.w = fmaf(m.w, f[j], e[j].w);
+        at[(s0 + j) * step] = m;
       }
   }
 }

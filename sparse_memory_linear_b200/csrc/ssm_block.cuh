@@ -78,47 +78,9 @@ constexpr float SB_LOG2E = 1.4426950408889634f;
 struct SsmBlockArgs {
   SsmArgs a;
   CUtensorMap mq, mk, mv;
-  int seg_blocks;   // blocks of a segment
+  SsmSplit sp;      // segments of whole blocks
   int ptiles;       // 64-column tiles of d_v
-  float* starts;    // [items, H, N, P]: the state before each segment of a split sequence
-  float* decays;    // [items, H]: the segment's whole decay
 };
-
-// The (sequence, segment) of work item `item`: a sequence of n rows has max(1, ceil(n / seg))
-// segments.  Called by one warp; false past the last.
-__device__ __forceinline__ bool ssm_find_item(const SeqBounds& seq, long long item, long long seg,
-                                              int* b_out, long long* s_out) {
-  if (!seq.cu) {
-    const long long per = seq.T > 0 ? (seq.T + seg - 1) / seg : 1;
-    *b_out = (int)(item / per);
-    *s_out = item % per;
-    return *b_out < seq.B;
-  }
-  const int lane = threadIdx.x & 31;
-  for (int b0 = 0; b0 < seq.B; b0 += 32) {
-    const int b = b0 + lane;
-    long long n = 0;
-    if (b < seq.B) {
-      const long long len = seq.end(b) - seq.start(b);
-      n = len > 0 ? (len + seg - 1) / seg : 1;
-    }
-    long long upto = n;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const long long o = __shfl_up_sync(FULL_MASK, upto, s);
-      if (lane >= s) upto += o;
-    }
-    const unsigned hit = __ballot_sync(FULL_MASK, upto > item);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      *b_out = b0 + l;
-      *s_out = item - __shfl_sync(FULL_MASK, upto - n, l);
-      return true;
-    }
-    item -= __shfl_sync(FULL_MASK, upto, 31);
-  }
-  return false;
-}
 
 // A block's step sizes and decay sums, by one warp: lane l holds tokens 4 l .. 4 l + 3.
 struct SsmSums {
@@ -209,7 +171,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   const long long item = blockIdx.x / per_item;
   const int hp = blockIdx.x % per_item, h = hp / ba.ptiles, p0 = hp % ba.ptiles * SB_P;
   const int g = h / (a.H / a.G);
-  const long long seg_rows = (long long)ba.seg_blocks * SB_L;
+  const long long seg_rows = ba.sp.seg_rows;
   if (warp == 0) {
     int b = 0;
     long long s = 0;
@@ -487,7 +449,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     float* const mrow = Mp + (size_t)n * a.P + p0;
     const bool split = seq1 - seq0 > seg_rows;
     const float* const from =
-        split ? ba.starts + (((size_t)item * a.H + h) * a.N + n) * a.P + p0 : mrow;
+        split ? ba.sp.starts + (((size_t)item * a.H + h) * a.N + n) * a.P + p0 : mrow;
     float2 st[SB_P / 2];
 #pragma unroll
     for (int i = 0; i < SB_P; i += 4) {
@@ -774,10 +736,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 }
 
 // ------------------------------------------------------------------------ split sequences
-// With few (sequence, head, tile) CTAs a sequence is cut into segments that are scanned at the
-// same time, each from the state before it.  Those states come from one more pass that makes
-// each segment's own contribution, dM over all its tokens at once (this kernel: one product,
-// no state to carry), and a short chain over the segments (ssm_chain_kernel).
+// The first pass of a split (SsmSplit): each segment's own contribution, dM over all its tokens
+// at once; one product, no state to carry.
 //
 // A segment's contribution is summed from its last block to its first, so that every token's
 // weight, its decay up to the segment's end, is known when its block is read, and all blocks
@@ -811,7 +771,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
   const long long item = blockIdx.x / per_item;
   const int hp = blockIdx.x % per_item, h = hp / ba.ptiles, p0 = hp % ba.ptiles * SB_P;
   const int g = h / (a.H / a.G);
-  const long long seg_rows = (long long)ba.seg_blocks * SB_L;
+  const long long seg_rows = ba.sp.seg_rows;
   if (warp == 0) {
     int b = 0;
     long long s = 0;
@@ -827,7 +787,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
   if (!s_item_ok) return;
   const long long row0 = a.seq.start(s_b) + s_seg * seg_rows;
   if (row0 + seg_rows >= a.seq.end(s_b)) return;  // nothing follows the last segment
-  const int nb = ba.seg_blocks;                   // all whole
+  const int nb = (int)(seg_rows / SB_L);          // all whole
   const int npanels = a.N > 64 ? 2 : 1;
 
   if (warp == 0) tmem_alloc(base + SG_TMEM_PTR, 128);
@@ -890,7 +850,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
       const int n = tid, pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;
       const uint32_t lanes = (uint32_t)(warp * 32) << 16;
       // the state before the next segment gets this one's contribution
-      float* to = ba.starts + (((size_t)(item + 1) * a.H + h) * a.N + n) * a.P + p0;
+      float* to = ba.sp.starts + (((size_t)(item + 1) * a.H + h) * a.N + n) * a.P + p0;
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
         float r1[16], r2[16];
@@ -977,57 +937,12 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(GB_PREP + (c & 1)));
     }
-    if (lane == 0 && p0 == 0) ba.decays[item * a.H + h] = exp2f(carry);
+    if (lane == 0 && p0 == 0) ba.sp.decays[item * a.H + h] = exp2f(carry);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_free(tm, 128);
-}
-
-// The states before the segments of a split sequence, from the first on: what the sequence
-// starts with, then each segment's decay and contribution.  A block per (sequence, head, 1024
-// state values).
-__global__ void __launch_bounds__(256) ssm_chain_kernel(const __grid_constant__ SsmBlockArgs ba) {
-  __shared__ long long s_first;
-  const SsmArgs& a = ba.a;
-  const int b = blockIdx.x, h = blockIdx.y, i = blockIdx.z * 256 + threadIdx.x;
-  const long long seg = (long long)ba.seg_blocks * SB_L, len = a.seq.end(b) - a.seq.start(b);
-  if (len <= seg) return;
-  if (threadIdx.x == 0) s_first = 0;
-  __syncthreads();
-  if (!a.seq.cu) {
-    if (threadIdx.x == 0) s_first = b * ((a.seq.T + seg - 1) / seg);
-  } else {
-    long long items = 0;
-    for (int e = threadIdx.x; e < b; e += 256) {
-      const long long n = a.seq.end(e) - a.seq.start(e);
-      items += n > 0 ? (n + seg - 1) / seg : 1;
-    }
-    if (items)
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s_first), (unsigned long long)items);
-  }
-  __syncthreads();
-  const int n4 = a.N * a.P / 4;
-  if (i >= n4) return;
-  const long long first = s_first;
-  const int segs = (int)((len + seg - 1) / seg);
-  const size_t step = (size_t)a.H * n4;
-  float4* at = reinterpret_cast<float4*>(ba.starts) + ((size_t)first * a.H + h) * n4 + i;
-  const float* decay = ba.decays + first * a.H + h;
-  float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (!a.from_zero) m = reinterpret_cast<const float4*>(a.M)[((size_t)b * a.H + h) * n4 + i];
-  at[0] = m;
-#pragma unroll 4
-  for (int s = 1; s < segs; ++s) {
-    const float4 e = at[s * step];
-    const float f = decay[(size_t)(s - 1) * a.H];
-    m.x = fmaf(m.x, f, e.x);
-    m.y = fmaf(m.y, f, e.y);
-    m.z = fmaf(m.z, f, e.z);
-    m.w = fmaf(m.w, f, e.w);
-    at[s * step] = m;
-  }
 }
 
 }  // namespace sdm

@@ -199,30 +199,33 @@ def test_ssm_packed(sdm, dt, lens, init):
     assert (y[:before] == 7).all() and (y[before + n:] == 7).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T,H,N,P,init", [
     (1, 5000, 2, 128, 64, "continue"), (2, 2437, 3, 64, 128, "zero"), (1, 4096, 1, 16, 40, "continue"),
+    (1, 1500, 1, 200, 24, "continue"),
 ])
-def test_ssm_long(sdm, B, T, H, N, P, init):
+def test_ssm_long(sdm, dt, B, T, H, N, P, init):
     """Prompts that are cut into segments (few heads, many blocks)."""
-    i, M = ssm_inputs(gen(T), (B, T), H, 1, N, P, torch.bfloat16, True, True, B)
+    i, M = ssm_inputs(gen(T), (B, T), H, 1, N, P, TYPES[dt], True, True, B)
     M0 = d64(M) if init == "continue" else torch.zeros_like(d64(M))
     y = sdm.sdm_ssm_forward(M=M, init=init, **i)
-    ry, rM, yb, Mb = ssm_ref(i, M0, [T] * B, "bf16")
+    ry, rM, yb, Mb = ssm_ref(i, M0, [T] * B, dt)
     ref.check(y.reshape(B * T, H, P), ry, yb, "y")
     ref.check(M, rM, Mb, "M")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("init", ["zero", "continue"])
 @pytest.mark.parametrize("lens", [[3000, 1, 0, 700, 1280, 128, 129], [0, 6000]])
-def test_ssm_long_packed(sdm, lens, init):
+def test_ssm_long_packed(sdm, dt, lens, init):
     """Packed batches with sequences of several segments next to short and empty ones."""
     B, H, N, P, n = len(lens), 2, 128, 64, sum(lens)
-    i, M = ssm_inputs(gen(n), (n + 3,), H, 2, N, P, torch.bfloat16, True, True, B)
+    i, M = ssm_inputs(gen(n), (n + 3,), H, 2, N, P, TYPES[dt], True, True, B)
     M0 = d64(M) if init == "continue" else torch.zeros_like(d64(M))
     y = torch.full_like(i["v"], 7.0)
     sdm.sdm_ssm_forward(M=M, init=init, cu=cu_of(lens), y=y, **i)
     own = {x: (z[:n] if x in ("k", "q", "v", "dt", "gate") else z) for x, z in i.items()}
-    ry, rM, yb, Mb = ssm_ref(own, M0, lens, "bf16")
+    ry, rM, yb, Mb = ssm_ref(own, M0, lens, dt)
     ref.check(y[:n], ry, yb, "y")
     ref.check(M, rM, Mb, "M")
     assert (y[n:] == 7).all()
