@@ -378,8 +378,9 @@ typedef struct {
     int64_t k_stride, q_stride, v_stride, dt_stride, gate_stride;
 } sdm_ssm_shape;
 
-/* Bytes of scratch that sdm_ssm_forward needs for this shape, packed or not; 0 for an invalid
- * shape. */
+/* Bytes of scratch that sdm_ssm_forward needs for this shape on the calling device, packed or
+ * not: the states between the segments of long sequences.  0 where it needs none (and for an
+ * invalid shape, which the call refuses). */
 size_t sdm_ssm_workspace_size(sdm_ssm_shape shape);
 
 /*

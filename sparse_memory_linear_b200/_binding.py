@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -498,27 +499,32 @@ def sdm_state_unpack(codes, scales, d_v: int, fmt: str = "e4m3", *, out=None, st
 _DTYPES = {torch.float32: SDM_F32, torch.bfloat16: SDM_BF16}
 
 
-def _on_device(dev):
-    """The library launches on the calling thread's current device: a guard that makes it
-    the tensors' (None where it is already)."""
-    return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
 def _call(name, dev, stream, *args):
-    """Calls the entry point with the stream as its last argument, on the tensors' device."""
+    """Calls the entry point with the stream as its last argument, on the tensors' device: the
+    library launches on the calling thread's current one."""
     fn = getattr(_lib or library(), name)
+    index = dev.index
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        # the raw handle: a Stream object costs as much as the launch
+        stream = torch._C._cuda_getCurrentRawStream(index)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    guard = _on_device(dev)
-    if guard is None:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, int(stream))
     else:
-        with guard:
+        with torch.cuda.device(dev):
             rc = fn(*args, int(stream))
     if rc != 0:
         raise SdmError(rc, name)
+
+
+def _out(out, like, pitch, dtype):
+    """A contiguous output of `like`'s shape: the one given, or a new one."""
+    if out is not None:
+        return _like(out, "y", like.shape, dtype, like.device)
+    if pitch == 0:
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=dtype, device=like.device)
 
 
 def _addr(t):
@@ -616,10 +622,7 @@ def sdm_conv_forward(x, w, state=None, *, bias=None, init: str = "zero", act: st
         raise ValueError(f"w has shape {tuple(w.shape)}, expected [C, K]")
     K = w.shape[1]
     pitch = _pitch(x, "x", x.shape, x.dim() - 1, dt, dev)
-    if y is None:
-        y = torch.empty(x.shape, dtype=dt, device=dev)
-    else:
-        _like(y, "y", x.shape, dt, dev)
+    y = _out(y, x, pitch, dt)
     _like(state, "state", (B, K - 1, C), dt, dev)
     _call("sdm_conv_forward", dev, stream, x.data_ptr(), _param(w, "w", (C, K), dev),
           _param(bias, "bias", (C,), dev), _addr(state), _dense_init(init), ACT[act], _addr(cu),
@@ -637,10 +640,7 @@ def sdm_conv_step(x, w, state, *, bias=None, act: str = "silu", y=None, stream=N
     B, C = x.shape
     K = w.shape[1]
     pitch = _pitch(x, "x", x.shape, 1, dt, dev)
-    if y is None:
-        y = torch.empty(x.shape, dtype=dt, device=dev)
-    else:
-        _like(y, "y", x.shape, dt, dev)
+    y = _out(y, x, pitch, dt)
     _like(state, "state", (B, K - 1, C), dt, dev)
     _call("sdm_conv_step", dev, stream, x.data_ptr(), _param(w, "w", (C, K), dev),
           _param(bias, "bias", (C,), dev), state.data_ptr(), ACT[act], y.data_ptr(),
@@ -655,23 +655,27 @@ def _ssm_shape(k, q, v, dt, A, M, D, dt_bias, gate, y, softplus, B, T, dev, dtyp
     H, P = v.shape[-2:]
     G, N = k.shape[-2:]
     kshape = lead + (G, N)
+    v_pitch = _pitch(v, "v", v.shape, nl, dtype, dev)
     shape = SdmSsmShape(
         B, T, H, G, N, P, _DTYPES[dtype], 1 if softplus else 0,
-        _pitch(k, "k", kshape, nl, dtype, dev), _pitch(q, "q", kshape, nl, dtype, dev),
-        _pitch(v, "v", v.shape, nl, dtype, dev), _pitch(dt, "dt", lead + (H,), nl, dtype, dev),
+        _pitch(k, "k", kshape, nl, dtype, dev), _pitch(q, "q", kshape, nl, dtype, dev), v_pitch,
+        _pitch(dt, "dt", lead + (H,), nl, dtype, dev),
         _pitch(gate, "gate", v.shape, nl, dtype, dev) if gate is not None else 0)
     _like(M, "M", (B, H, N, P), torch.float32, dev)
     params = (_param(A, "A", (H,), dev), _param(dt_bias, "dt_bias", (H,), dev),
               _param(D, "D", (H,), dev))
-    if y is None:
-        y = torch.empty(v.shape, dtype=dtype, device=dev)
-    else:
-        _like(y, "y", v.shape, dtype, dev)
-    return shape, y, params
+    return shape, _out(y, v, v_pitch, dtype), params
 
 
 def sdm_ssm_workspace_size(shape: SdmSsmShape) -> int:
     return int(library().sdm_ssm_workspace_size(shape))
+
+
+@functools.lru_cache(maxsize=1024)
+def _ssm_scratch(index, *fields):
+    """sdm_ssm_workspace_size on device `index` (its answer depends on the device's size)."""
+    with torch.cuda.device(index):
+        return sdm_ssm_workspace_size(SdmSsmShape(*fields))
 
 
 def sdm_ssm_forward(k, q, v, dt, A, M, *, init: str = "zero", D=None, dt_bias=None,
@@ -689,11 +693,14 @@ def sdm_ssm_forward(k, q, v, dt, A, M, *, init: str = "zero", D=None, dt_bias=No
     shape, y, params = _ssm_shape(k, q, v, dt, A, M, D, dt_bias, gate, y, softplus, B, T, dev,
                                   dtype)
     if ws is None:
-        ws = torch.empty(max(sdm_ssm_workspace_size(shape), 1), dtype=torch.uint8, device=dev)
-    _need(ws, "ws", torch.uint8, dev)
+        need = _ssm_scratch(dev.index, B, T, shape.H, shape.G, shape.N, shape.d_v,
+                            shape.in_dtype)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _need(ws, "ws", torch.uint8, dev)
     _call("sdm_ssm_forward", dev, stream, k.data_ptr(), q.data_ptr(), v.data_ptr(),
           dt.data_ptr(), *params, M.data_ptr(), _dense_init(init), _addr(gate), ACT[act],
-          _addr(cu), y.data_ptr(), ws.data_ptr(), ws.numel(), shape)
+          _addr(cu), y.data_ptr(), _addr(ws), ws.numel() if ws is not None else 0, shape)
     return y
 
 
@@ -726,11 +733,11 @@ def sdm_block_norm(u, r, *, post_norm: bool = True, post_gamma=None, gate=None,
     _like(r, "r", u.shape, rdt, dev)
     _like(gate, "gate", u.shape, dtype, dev)
     if r_out is None:
-        r_out = torch.empty(u.shape, dtype=rdt, device=dev)
+        r_out = torch.empty_like(r)
     else:
         _like(r_out, "r_out", u.shape, rdt, dev)
     if n is None:
-        n = torch.empty(u.shape, dtype=dtype, device=dev) if want_n else None
+        n = torch.empty_like(u) if want_n else None
     else:
         _like(n, "n", u.shape, dtype, dev)
     _call("sdm_block_norm", dev, stream, u.data_ptr(), _addr(gate), ACT[act],

@@ -232,7 +232,7 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, c
   long long best = 1;
   double least = waves(seqs) * L * c.walk_us;
   const long long most = 6LL * c.slots / (seqs * ctas_per_item) + 1;  // more waves gain nothing
-  for (long long n = 2; n <= L && n <= most; ++n) {
+  for (long long n = 2; n <= L && n <= most; n += n < 16 ? 1 : n / 16) {
     const long long len = (L + n - 1) / n;
     if ((L + len - 1) / len != n) continue;
     const double t = waves(seqs * n) * len * c.walk_us + waves(seqs * (n - 1)) * len * c.pre_us +
@@ -370,7 +370,7 @@ size_t sdm_ssm_workspace_size(sdm_ssm_shape shape) {
   SsmArgs a;
   DeviceInfo* di;
   if (!ssm_args(shape, false, &a)) return 0;
-  size_t need = WS_ALIGN;
+  size_t need = 0;
   // without a device (sizes asked for ahead of time) a B200's number of multiprocessors
   const int sms = device_info(&di) == SDM_OK ? di->sms : 148;
   for (const bool packed : {false, true}) {
@@ -393,8 +393,8 @@ sdm_status sdm_ssm_forward(const void* k, const void* q, const void* v, const vo
   const long long R = cu ? s.T : (long long)s.B * s.T;
   if (!ssm_pointers(s, R, k, q, v, dt, A, dt_bias, D, M, gate, act, cu, y, &a))
     return SDM_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < sdm_ssm_workspace_size(s) ||
-      reinterpret_cast<uintptr_t>(ws) % WS_ALIGN != 0)
+  const size_t need = sdm_ssm_workspace_size(s);
+  if (need && (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % WS_ALIGN != 0))
     return SDM_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (R == 0) {

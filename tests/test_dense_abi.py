@@ -110,11 +110,13 @@ def test_ssm_refuses_more(sdm):
     refused(sdm, 1, ssm(sdm, init=0))
     refused(sdm, 1, ssm(sdm, shape=dict(T=-1)))
     refused(sdm, 1, ssm(sdm, cu=at(11) + 1))
-    need = sdm.sdm_ssm_workspace_size(sdm.SdmSsmShape(2, 16, 4, 2, 64, 64, 1, 1, 0, 0, 0, 0, 0))
-    assert need > 0
-    refused(sdm, 1, ssm(sdm, ws=None))
-    refused(sdm, 1, ssm(sdm, ws=at(10) + 16))
-    refused(sdm, 1, ssm(sdm, ws_bytes=need - 1))
+    # a long prompt of few heads is cut into segments: scratch for the states between them
+    long = dict(T=8192)
+    need = sdm.sdm_ssm_workspace_size(sdm.SdmSsmShape(2, 8192, 4, 2, 64, 64, 1, 1, 0, 0, 0, 0, 0))
+    assert need >= 2 * 2 * 4 * 64 * 64 * 4
+    refused(sdm, 1, ssm(sdm, shape=long, ws=None))
+    refused(sdm, 1, ssm(sdm, shape=long, ws=at(10) + 16))
+    refused(sdm, 1, ssm(sdm, shape=long, ws_bytes=need - 1))
     assert sdm.sdm_ssm_workspace_size(sdm.SdmSsmShape(2, 16, 4, 3, 64, 64, 1, 1, 0, 0, 0, 0,
                                                       0)) == 0
 

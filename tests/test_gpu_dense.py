@@ -524,7 +524,10 @@ def test_binding_refuses(sdm):
     bad(cu=torch.zeros(3, dtype=torch.int32, device=DEV))
     bad(y=i["v"])            # y over an input
     bad(gate=i["gate"].cpu())
-    bad(ws=torch.empty(1, dtype=torch.uint8, device=DEV))
+    bad(ws=torch.empty(1, dtype=torch.int32, device=DEV))
+    long, M8 = ssm_inputs(g, (2, 8192), 4, 2, 64, 64, torch.bfloat16, False, False, 2)
+    with pytest.raises(sdm.SdmError):  # scratch too small for the states between segments
+        sdm.sdm_ssm_forward(M=M8, ws=torch.empty(1024, dtype=torch.uint8, device=DEV), **long)
     x, w = randn(g, 2, 9, 64), randn(g, 64, 4)
     for args, kw in (((x, w[:, :3]), dict(init="continue")), ((x.half(), w), {}),
                      ((x, w.to(torch.bfloat16)), {}), ((x, randn(g, 64, 5)), {}),
