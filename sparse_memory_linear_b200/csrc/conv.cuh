@@ -6,7 +6,7 @@
 // zero.
 #pragma once
 
-#include "common.cuh"
+#include "fastmath.cuh"
 
 namespace sdm {
 
@@ -17,6 +17,12 @@ struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
   uint4 raw;
+  __device__ __forceinline__ void get2(float2 f[4]) const {
+    f[0] = unpack_bf16(raw.x);
+    f[1] = unpack_bf16(raw.y);
+    f[2] = unpack_bf16(raw.z);
+    f[3] = unpack_bf16(raw.w);
+  }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     raw = *reinterpret_cast<const uint4*>(p);
   }
@@ -43,6 +49,12 @@ struct Vec8<__nv_bfloat16> {
 template <>
 struct Vec8<float> {
   float4 a, b;
+  __device__ __forceinline__ void get2(float2 f[4]) const {
+    f[0] = make_float2(a.x, a.y);
+    f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y);
+    f[3] = make_float2(b.z, b.w);
+  }
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
@@ -116,34 +128,53 @@ struct ConvArgs {
   long long x_stride, tiles;
 };
 
+// A thread's eight channels: weights by tap, as pairs of channels, and the last K - 1 inputs.
 template <typename T, int K>
-struct ConvWeights {
-  float w[K][8], bias[8];
-  __device__ __forceinline__ void load(const float* wp, const float* bp, int c0) {
+struct ConvLane {
+  float2 w[K][4], bias[4], win[K][4];
+  __device__ __forceinline__ void load_weights(const float* wp, const float* bp, int c0) {
+    float f[8 * K];  // [channel][tap], contiguous
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-#pragma unroll
-      for (int j = 0; j < K; ++j) w[j][e] = __ldg(wp + (size_t)(c0 + e) * K + j);
-      bias[e] = bp ? __ldg(bp + c0 + e) : 0.0f;
+    for (int i = 0; i < 2 * K; ++i) {
+      const float4 t = __ldg(reinterpret_cast<const float4*>(wp + (size_t)c0 * K) + i);
+      f[4 * i] = t.x;
+      f[4 * i + 1] = t.y;
+      f[4 * i + 2] = t.z;
+      f[4 * i + 3] = t.w;
     }
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[j][e] = make_float2(f[2 * e * K + j], f[(2 * e + 1) * K + j]);
+    float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
+    if (bp) {
+      b0 = __ldg(reinterpret_cast<const float4*>(bp + c0));
+      b1 = __ldg(reinterpret_cast<const float4*>(bp + c0) + 1);
+    }
+    bias[0] = make_float2(b0.x, b0.y);
+    bias[1] = make_float2(b0.z, b0.w);
+    bias[2] = make_float2(b1.x, b1.y);
+    bias[3] = make_float2(b1.z, b1.w);
   }
-  // One output row from its K input rows (oldest first).
-  __device__ __forceinline__ void row(const Vec8<T> in[K], int act, T* out) const {
-    float acc[8];
+  // The next input: its output row, and the window moves up by one.
+  __device__ __forceinline__ void row(const Vec8<T>& in, int act, T* out) {
+    in.get2(win[K - 1]);
+    float o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = bias[e];
+    for (int e = 0; e < 4; ++e) {
+      float2 acc = bias[e];
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      float f[8];
-      in[j].get(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j][e], f[e], acc[e]);
+      for (int j = 0; j < K; ++j) acc = fma2(w[j][e], win[j][e], acc);
+      o[2 * e] = fast_gate_act(acc.x, act);
+      o[2 * e + 1] = fast_gate_act(acc.y, act);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = gate_act(acc[e], act);
-    Vec8<T> o;
-    o.set(acc);
-    o.store(out);
+    for (int j = 0; j + 1 < K; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) win[j][e] = win[j + 1][e];
+    Vec8<T> r;
+    r.set(o);
+    r.store(out);
   }
 };
 
@@ -152,7 +183,7 @@ struct ConvWeights {
 // rewritten in place; so the thread whose rows hold a sequence's first row also computes the
 // rest of those K - 1 rows and writes the new state, and no other thread touches the state.
 template <typename T, int K>
-__global__ void __launch_bounds__(256) conv_forward_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(128) conv_forward_kernel(ConvArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) a.seq.check();
@@ -163,31 +194,30 @@ __global__ void __launch_bounds__(256) conv_forward_kernel(ConvArgs a) {
   const T* x = static_cast<const T*>(a.x) + c0;
   T* y = static_cast<T*>(a.y) + c0;
   T* state = a.state ? static_cast<T*>(a.state) + c0 : nullptr;
-  ConvWeights<T, K> cw;
-  cw.load(a.w, a.bias, c0);
+  ConvLane<T, K> lane;
+  lane.load_weights(a.w, a.bias, c0);
   const long long r0 = tile * a.rows_per_thread;
   const bool last_tile = tile == a.tiles - 1;
   const long long r1 = last_tile ? a.seq.R : r0 + a.rows_per_thread;
 
-  auto walk = [&](long long r, long long end, Vec8<T> win[K]) {
-    // win[0..K-2]: the K - 1 rows before r
-    for (; r + 4 <= end; r += 4) {
+  auto walk = [&](long long r, long long end) {
+    const T* xr = x + r * a.x_stride;
+    T* yr = y + r * a.C;
+    for (; r + 4 <= end; r += 4) {  // four rows on their way at a time
       Vec8<T> nx[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) nx[i].load(x + (r + i) * a.x_stride);
+      for (int i = 0; i < 4; ++i) nx[i].load(xr + i * a.x_stride);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        win[K - 1] = nx[i];
-        cw.row(win, a.act, y + (r + i) * a.C);
-#pragma unroll
-        for (int j = 0; j + 1 < K; ++j) win[j] = win[j + 1];
-      }
+      for (int i = 0; i < 4; ++i) lane.row(nx[i], a.act, yr + (size_t)i * a.C);
+      xr += 4 * a.x_stride;
+      yr += (size_t)4 * a.C;
     }
     for (; r < end; ++r) {
-      win[K - 1].load(x + r * a.x_stride);
-      cw.row(win, a.act, y + r * a.C);
-#pragma unroll
-      for (int j = 0; j + 1 < K; ++j) win[j] = win[j + 1];
+      Vec8<T> nx;
+      nx.load(xr);
+      lane.row(nx, a.act, yr);
+      xr += a.x_stride;
+      yr += a.C;
     }
   };
 
@@ -197,16 +227,19 @@ __global__ void __launch_bounds__(256) conv_forward_kernel(ConvArgs a) {
     long long r = s0 + K - 1 > r0 ? s0 + K - 1 : r0;
     const long long end = e0 < r1 ? e0 : r1;
     if (s0 < r0 && r < end) {
-      Vec8<T> win[K];
 #pragma unroll
-      for (int j = 0; j + 1 < K; ++j) win[j].load(x + (r - (K - 1) + j) * a.x_stride);
-      walk(r, end, win);
+      for (int j = 0; j + 1 < K; ++j) {
+        Vec8<T> t;
+        t.load(x + (r - (K - 1) + j) * a.x_stride);
+        t.get2(lane.win[j]);
+      }
+      walk(r, end);
     }
   }
   for (; b < a.seq.B; ++b) {
     const long long s0 = a.seq.start(b), e0 = a.seq.end(b);
     if (s0 >= r1 && !last_tile) break;
-    Vec8<T> win[K];
+    Vec8<T> win[K - 1];
 #pragma unroll
     for (int j = 0; j + 1 < K; ++j) {
       if (a.from_zero)
@@ -231,9 +264,11 @@ __global__ void __launch_bounds__(256) conv_forward_kernel(ConvArgs a) {
         t.store(state + ((size_t)b * (K - 1) + j) * a.C);
       }
     }
+#pragma unroll
+    for (int j = 0; j + 1 < K; ++j) win[j].get2(lane.win[j]);
     long long end = s0 + K - 1 > r1 ? s0 + K - 1 : r1;
     if (e0 < end) end = e0;
-    walk(s0, end, win);
+    walk(s0, end);
   }
 }
 
@@ -252,11 +287,14 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
 #pragma unroll
   for (int j = 0; j + 1 < K; ++j) win[j].load(state + (size_t)j * a.C);
   win[K - 1].load(static_cast<const T*>(a.x) + b * a.x_stride + c0);
-  ConvWeights<T, K> cw;
-  cw.load(a.w, a.bias, c0);
+  ConvLane<T, K> lane;
+  lane.load_weights(a.w, a.bias, c0);
 #pragma unroll
-  for (int j = 0; j + 1 < K; ++j) win[j + 1].store(state + (size_t)j * a.C);
-  cw.row(win, a.act, static_cast<T*>(a.y) + (size_t)b * a.C + c0);
+  for (int j = 0; j + 1 < K; ++j) {
+    win[j].get2(lane.win[j]);
+    win[j + 1].store(state + (size_t)j * a.C);
+  }
+  lane.row(win[K - 1], a.act, static_cast<T*>(a.y) + (size_t)b * a.C + c0);
 }
 
 }  // namespace sdm

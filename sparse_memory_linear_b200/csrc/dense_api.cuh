@@ -44,7 +44,7 @@ bool conv_shape_ok(const sdm_conv_shape& s, bool step) {
 
 template <typename T>
 cudaError_t launch_conv(bool step, int K, unsigned blocks, cudaStream_t st, const ConvArgs& a) {
-  const dim3 grid(blocks), block(step ? 128 : 256);
+  const dim3 grid(blocks), block(128);
   if (step) {
     if (K == 2) return launch_pdl<true>(conv_step_kernel<T, 2>, grid, block, 0, st, a);
     if (K == 3) return launch_pdl<true>(conv_step_kernel<T, 3>, grid, block, 0, st, a);
@@ -94,10 +94,14 @@ sdm_status conv_run(const void* x, const float* w, const float* bias, void* stat
   a.from_zero = init == SDM_INIT_ZERO;
   a.act = act;
   a.x_stride = pitch;
-  a.rows_per_thread = 16;
+  // rows of a thread: enough threads for four waves of a full device, at least four rows (a
+  // thread's weights and the K - 1 rows before its own are read once for all of them), at most 64
+  const long long threads = (long long)di->sms * 512 * 4;
+  a.rows_per_thread = 4;
+  while (a.rows_per_thread < 64 && R * a.cv > threads * a.rows_per_thread * 3 / 2)
+    a.rows_per_thread *= 2;
   a.tiles = step ? s.B : (R + a.rows_per_thread - 1) / a.rows_per_thread;
-  const int threads = step ? 128 : 256;
-  const long long blocks = (a.tiles * a.cv + threads - 1) / threads;
+  const long long blocks = (a.tiles * a.cv + 127) / 128;
   if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;
   ProfScope ps(SDM_KERNEL_CONV, st);
   if (s.in_dtype == SDM_BF16)
