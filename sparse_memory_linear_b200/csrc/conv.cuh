@@ -96,7 +96,9 @@ struct SeqBounds {
   // The first sequence that starts at row r or later (B: none).
   __device__ __forceinline__ int first_from(long long r) const {
     if (!cu) {
-      const long long b = (r + T - 1) / T;
+      // 32-bit division where it serves: the 64-bit one costs as much as several rows
+      const long long b = R < 0x7fffffffLL ? (long long)((unsigned)(r + T - 1) / (unsigned)T)
+                                           : (r + T - 1) / T;
       return b > B ? B : (int)b;
     }
     int lo = 0, hi = B;
@@ -123,19 +125,62 @@ struct ConvArgs {
   void* state;  // [B, K - 1, C]; may be null when from_zero
   void* y;
   SeqBounds seq;
-  int C, cv;  // channels, C / 8
+  int C, cv;  // channels, C / 4
   int from_zero, act, rows_per_thread;
   long long x_stride, tiles;
 };
 
-// A thread's eight channels: weights by tap, as pairs of channels, and the last K - 1 inputs.
+// Four values: 8 or 16 bytes.
+template <typename T>
+struct Vec4;
+
+template <>
+struct Vec4<__nv_bfloat16> {
+  uint2 raw;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    raw = *reinterpret_cast<const uint2*>(p);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint2*>(p) = raw;
+  }
+  __device__ __forceinline__ void zero() { raw = make_uint2(0, 0); }
+  __device__ __forceinline__ void get2(float2 f[2]) const {
+    f[0] = unpack_bf16(raw.x);
+    f[1] = unpack_bf16(raw.y);
+  }
+  __device__ __forceinline__ void set2(const float2 f[2]) {
+    raw = make_uint2(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y));
+  }
+};
+
+template <>
+struct Vec4<float> {
+  float4 raw;
+  __device__ __forceinline__ void load(const float* p) {
+    raw = *reinterpret_cast<const float4*>(p);
+  }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = raw; }
+  __device__ __forceinline__ void zero() { raw = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get2(float2 f[2]) const {
+    f[0] = make_float2(raw.x, raw.y);
+    f[1] = make_float2(raw.z, raw.w);
+  }
+  __device__ __forceinline__ void set2(const float2 f[2]) {
+    raw = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  }
+};
+
+// A thread's four channels: weights by tap, as pairs of channels, and the last K - 1 inputs.
+// With eight channels a thread held 128 registers, and 512 threads a multiprocessor kept too few
+// loads on their way: 48 us against 33 for 4 x 8192 x 1280 bf16.
+
 template <typename T, int K>
 struct ConvLane {
-  float2 w[K][4], bias[4], win[K][4];
+  float2 w[K][2], bias[2], win[K][2];
   __device__ __forceinline__ void load_weights(const float* wp, const float* bp, int c0) {
-    float f[8 * K];  // [channel][tap], contiguous
+    float f[4 * K];  // [channel][tap], contiguous
 #pragma unroll
-    for (int i = 0; i < 2 * K; ++i) {
+    for (int i = 0; i < K; ++i) {
       const float4 t = __ldg(reinterpret_cast<const float4*>(wp + (size_t)c0 * K) + i);
       f[4 * i] = t.x;
       f[4 * i + 1] = t.y;
@@ -145,52 +190,47 @@ struct ConvLane {
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[j][e] = make_float2(f[2 * e * K + j], f[(2 * e + 1) * K + j]);
-    float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
-    if (bp) {
-      b0 = __ldg(reinterpret_cast<const float4*>(bp + c0));
-      b1 = __ldg(reinterpret_cast<const float4*>(bp + c0) + 1);
-    }
-    bias[0] = make_float2(b0.x, b0.y);
-    bias[1] = make_float2(b0.z, b0.w);
-    bias[2] = make_float2(b1.x, b1.y);
-    bias[3] = make_float2(b1.z, b1.w);
+      for (int e = 0; e < 2; ++e) w[j][e] = make_float2(f[2 * e * K + j], f[(2 * e + 1) * K + j]);
+    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (bp) b = __ldg(reinterpret_cast<const float4*>(bp + c0));
+    bias[0] = make_float2(b.x, b.y);
+    bias[1] = make_float2(b.z, b.w);
   }
   // The next input: its output row, and the window moves up by one.
-  __device__ __forceinline__ void row(const Vec8<T>& in, int act, T* out) {
+  __device__ __forceinline__ void row(const Vec4<T>& in, int act, T* out) {
     in.get2(win[K - 1]);
-    float o[8];
+    float2 o[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 2; ++e) {
       float2 acc = bias[e];
 #pragma unroll
       for (int j = 0; j < K; ++j) acc = fma2(w[j][e], win[j][e], acc);
-      o[2 * e] = fast_gate_act(acc.x, act);
-      o[2 * e + 1] = fast_gate_act(acc.y, act);
+      o[e] = make_float2(fast_gate_act(acc.x, act), fast_gate_act(acc.y, act));
     }
 #pragma unroll
     for (int j = 0; j + 1 < K; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) win[j][e] = win[j + 1][e];
-    Vec8<T> r;
-    r.set(o);
+      for (int e = 0; e < 2; ++e) win[j][e] = win[j + 1][e];
+    Vec4<T> r;
+    r.set2(o);
     r.store(out);
   }
 };
 
-// One thread walks `rows_per_thread` rows of eight channels with the last K - 1 inputs in
+// One thread walks `rows_per_thread` rows of four channels with the last K - 1 inputs in
 // registers.  The first K - 1 rows of a sequence need its kept state, and the state is
 // rewritten in place; so the thread whose rows hold a sequence's first row also computes the
 // rest of those K - 1 rows and writes the new state, and no other thread touches the state.
 template <typename T, int K>
-__global__ void __launch_bounds__(128) conv_forward_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(128, 7) conv_forward_kernel(ConvArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0) a.seq.check();
   const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long tile = idx / a.cv;
+  const long long tile =
+      idx < 0xffffffffLL ? (long long)((unsigned)idx / (unsigned)a.cv) : idx / a.cv;
   if (tile >= a.tiles) return;
-  const int c0 = (int)(idx - tile * a.cv) * 8;
+  const int c0 = (int)(idx - tile * a.cv) * 4;
   const T* x = static_cast<const T*>(a.x) + c0;
   T* y = static_cast<T*>(a.y) + c0;
   T* state = a.state ? static_cast<T*>(a.state) + c0 : nullptr;
@@ -203,17 +243,18 @@ __global__ void __launch_bounds__(128) conv_forward_kernel(ConvArgs a) {
   auto walk = [&](long long r, long long end) {
     const T* xr = x + r * a.x_stride;
     T* yr = y + r * a.C;
-    for (; r + 4 <= end; r += 4) {  // four rows on their way at a time
-      Vec8<T> nx[4];
+    constexpr int CONV_ROWS = 16 / (int)sizeof(T);  // on their way at a time: 64 bytes
+    for (; r + CONV_ROWS <= end; r += CONV_ROWS) {
+      Vec4<T> nx[CONV_ROWS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) nx[i].load(xr + i * a.x_stride);
+      for (int i = 0; i < CONV_ROWS; ++i) nx[i].load(xr + i * a.x_stride);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lane.row(nx[i], a.act, yr + (size_t)i * a.C);
-      xr += 4 * a.x_stride;
-      yr += (size_t)4 * a.C;
+      for (int i = 0; i < CONV_ROWS; ++i) lane.row(nx[i], a.act, yr + (size_t)i * a.C);
+      xr += CONV_ROWS * a.x_stride;
+      yr += (size_t)CONV_ROWS * a.C;
     }
     for (; r < end; ++r) {
-      Vec8<T> nx;
+      Vec4<T> nx;
       nx.load(xr);
       lane.row(nx, a.act, yr);
       xr += a.x_stride;
@@ -229,7 +270,7 @@ __global__ void __launch_bounds__(128) conv_forward_kernel(ConvArgs a) {
     if (s0 < r0 && r < end) {
 #pragma unroll
       for (int j = 0; j + 1 < K; ++j) {
-        Vec8<T> t;
+        Vec4<T> t;
         t.load(x + (r - (K - 1) + j) * a.x_stride);
         t.get2(lane.win[j]);
       }
@@ -239,7 +280,7 @@ __global__ void __launch_bounds__(128) conv_forward_kernel(ConvArgs a) {
   for (; b < a.seq.B; ++b) {
     const long long s0 = a.seq.start(b), e0 = a.seq.end(b);
     if (s0 >= r1 && !last_tile) break;
-    Vec8<T> win[K - 1];
+    Vec4<T> win[K - 1];
 #pragma unroll
     for (int j = 0; j + 1 < K; ++j) {
       if (a.from_zero)
@@ -251,7 +292,7 @@ __global__ void __launch_bounds__(128) conv_forward_kernel(ConvArgs a) {
 #pragma unroll
       for (int j = 0; j + 1 < K; ++j) {
         const long long r = e0 - (K - 1) + j;
-        Vec8<T> t;
+        Vec4<T> t;
         if (r >= s0) {
           t.load(x + r * a.x_stride);
         } else {
@@ -273,7 +314,7 @@ __global__ void __launch_bounds__(128) conv_forward_kernel(ConvArgs a) {
 }
 
 // One token: the state's K - 1 inputs and the new one give the output, and the state moves up
-// by one.  A thread per eight channels of a sequence.
+// by one.  A thread per four channels of a sequence.
 template <typename T, int K>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
   grid_dependency_wait();
@@ -281,9 +322,9 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
   const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long b = idx / a.cv;
   if (b >= a.seq.B) return;
-  const int c0 = (int)(idx - b * a.cv) * 8;
+  const int c0 = (int)(idx - b * a.cv) * 4;
   T* state = static_cast<T*>(a.state) + (size_t)b * (K - 1) * a.C + c0;
-  Vec8<T> win[K];
+  Vec4<T> win[K];
 #pragma unroll
   for (int j = 0; j + 1 < K; ++j) win[j].load(state + (size_t)j * a.C);
   win[K - 1].load(static_cast<const T*>(a.x) + b * a.x_stride + c0);

@@ -90,15 +90,15 @@ sdm_status conv_run(const void* x, const float* w, const float* bias, void* stat
   a.y = y;
   a.seq = SeqBounds{cu, s.B, step ? 1 : s.T, R};
   a.C = s.C;
-  a.cv = s.C / 8;
+  a.cv = s.C / 4;
   a.from_zero = init == SDM_INIT_ZERO;
   a.act = act;
   a.x_stride = pitch;
-  // rows of a thread: enough threads for four waves of a full device, at least four rows (a
-  // thread's weights and the K - 1 rows before its own are read once for all of them), at most 64
-  const long long threads = (long long)di->sms * 512 * 4;
-  a.rows_per_thread = 4;
-  while (a.rows_per_thread < 64 && R * a.cv > threads * a.rows_per_thread * 3 / 2)
+  // rows of a thread: enough threads for two waves of a full device, at least eight rows (a
+  // thread's weights and the K - 1 rows before its own are read once for all of them), at most 32
+  const long long threads = (long long)di->sms * 896 * 2;
+  a.rows_per_thread = 8;
+  while (a.rows_per_thread < 32 && R * a.cv > threads * a.rows_per_thread * 3 / 2)
     a.rows_per_thread *= 2;
   a.tiles = step ? s.B : (R + a.rows_per_thread - 1) / a.rows_per_thread;
   const long long blocks = (a.tiles * a.cv + 127) / 128;
