@@ -27,7 +27,8 @@ struct BlockNormArgs {
   float eps;
 };
 
-// Sum over the TPR threads of a row (TPR a multiple of 32; rows of a block side by side).
+// Sum over the TPR threads of a row (TPR a multiple of 32; rows of a block side by side).  `part`
+// is written once per call: calls that may overlap need a part of their own.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
@@ -45,106 +46,130 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
+// Eight values of a parameter, 1 where there is none.
+__device__ __forceinline__ void load_param(const float* p, int v, float2 g[4]) {
+  if (p) {
+    Vec8<float> t;
+    t.load(p + 8 * v);
+    t.get2(g);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) g[e] = make_float2(1.0f, 1.0f);
+  }
+}
+
 // TPR threads per row, each with up to NV groups of eight values in registers; 256 threads (or
-// TPR, if more) to a block, blocks stride over the rows.
+// TPR, if more) to a block, blocks stride over the rows.  With one group a thread (rows of up to
+// 4096 values) the parameters stay in registers, 12 of the 26 bytes a value that would cross
+// the L1 otherwise, and the next row is on its way while this one is summed.  The sums keep two
+// sets of partial sums, so that two barriers a row are enough.
 template <typename T, typename TR, int TPR, int NV>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) block_norm_kernel(BlockNormArgs a) {
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? (TPR > 256 ? 1 : 2) : 1)
+    block_norm_kernel(BlockNormArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int THREADS = TPR > 256 ? TPR : 256;
   constexpr int RPB = THREADS / TPR;
-  __shared__ float part[2][THREADS / 32];
+  constexpr bool KEEP = NV == 1;
+  __shared__ float part[2][2][THREADS / 32];
   const int lane = threadIdx.x % TPR;
   const int nvec = a.D / 8;
-  for (long long row0 = (long long)blockIdx.x * RPB; row0 < a.rows;
-       row0 += (long long)gridDim.x * RPB) {
-    const long long row = row0 + threadIdx.x / TPR;
-    const bool on = row < a.rows;
-    const size_t base = (size_t)row * a.D;
-    float f[NV][8], r[NV][8];
-    float ss = 0.0f;
+  const float inv_d = 1.0f / (float)a.D;
+  float2 gpost[4], gscale[4], gpre[4];
+  if (KEEP && lane < nvec) {
+    load_param(a.post ? a.post_gamma : nullptr, lane, gpost);
+    load_param(a.scale, lane, gscale);
+    load_param(a.pre_gamma, lane, gpre);
+  }
+  struct Row {  // as stored: a third of the registers that the values take
+    Vec8<T> u[NV], z[NV];
+    Vec8<TR> r[NV];
+  };
+  Row next;
+  auto fetch = [&](long long row, Row& o) {
+    if (row >= a.rows) return;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * TPR;
+      if (v >= nvec) continue;
+      const size_t at = (size_t)row * a.D + 8 * v;
+      o.u[i].load(static_cast<const T*>(a.u) + at);
+      o.r[i].load(static_cast<const TR*>(a.r) + at);
+      if (a.gate) o.z[i].load(static_cast<const T*>(a.gate) + at);
+    }
+  };
+  const long long step = (long long)gridDim.x * RPB;
+  if (KEEP) fetch((long long)blockIdx.x * RPB + threadIdx.x / TPR, next);
+  int turn = 0;
+  for (long long row0 = (long long)blockIdx.x * RPB; row0 < a.rows; row0 += step, turn ^= 1) {
+    const long long row = row0 + threadIdx.x / TPR;
+    const bool on = row < a.rows;
+    const size_t base = (size_t)row * a.D;
+    Row cur;
+    if (KEEP) {
+      cur = next;
+      fetch(row + step, next);
+    } else {
+      fetch(row, cur);
+    }
+    float2 r[NV][4];
+    float ss = 0.0f;
+    if (a.post) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = r[i][e] = 0.0f;
-      if (on && v < nvec) {
-        Vec8<T> t;
-        Vec8<TR> tr;
-        t.load(static_cast<const T*>(a.u) + base + 8 * v);
-        tr.load(static_cast<const TR*>(a.r) + base + 8 * v);
-        t.get(f[i]);
-        tr.get(r[i]);
+      for (int i = 0; i < NV; ++i) {
+        if (!on || lane + i * TPR >= nvec) continue;
+        float2 f[4];
+        cur.u[i].get2(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(f[i][e], f[i][e], ss);
+        for (int e = 0; e < 4; ++e) {
+          ss = fmaf(f[e].x, f[e].x, ss);
+          ss = fmaf(f[e].y, f[e].y, ss);
+        }
       }
     }
     float inv = 1.0f;
-    if (a.post) inv = rsqrtf(row_sum<TPR>(ss, part[0]) / (float)a.D + a.eps);
+    if (a.post) inv = rsqrtf(row_sum<TPR>(ss, part[turn][0]) * inv_d + a.eps);
     ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = lane + i * TPR;
       if (!on || v >= nvec) continue;
-      if (a.post) {
-        float g[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = 1.0f;
-        if (a.post_gamma) {
-          Vec8<float> t;
-          t.load(a.post_gamma + 8 * v);
-          t.get(g);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * inv * g[e];
+      if (!KEEP) {
+        load_param(a.post ? a.post_gamma : nullptr, v, gpost);
+        load_param(a.scale, v, gscale);
       }
-      if (a.gate) {
-        Vec8<T> t;
-        float g[8];
-        t.load(static_cast<const T*>(a.gate) + base + 8 * v);
-        t.get(g);
+      float2 f[4], z[4];
+      cur.u[i].get2(f);
+      cur.r[i].get2(r[i]);
+      if (a.gate) cur.z[i].get2(z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] *= gate_act(g[e], a.act);
-      }
-      if (a.scale) {
-        Vec8<float> t;
-        float g[8];
-        t.load(a.scale + 8 * v);
-        t.get(g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] *= g[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        r[i][e] += f[i][e];
-        ss = fmaf(r[i][e], r[i][e], ss);
+      for (int e = 0; e < 4; ++e) {
+        float2 t = mul2(mul2(f[e], make_float2(inv, inv)), gpost[e]);
+        if (a.gate)
+          t = mul2(t, make_float2(fast_gate_act(z[e].x, a.act), fast_gate_act(z[e].y, a.act)));
+        r[i][e] = fma2(t, gscale[e], r[i][e]);
+        ss = fmaf(r[i][e].x, r[i][e].x, ss);
+        ss = fmaf(r[i][e].y, r[i][e].y, ss);
       }
       Vec8<TR> tr;
-      tr.set(r[i]);
+      tr.set2(r[i]);
       tr.store(static_cast<TR*>(a.r_out) + base + 8 * v);
     }
     if (a.n) {
-      inv = rsqrtf(row_sum<TPR>(ss, part[1]) / (float)a.D + a.eps);
+      inv = rsqrtf(row_sum<TPR>(ss, part[turn][1]) * inv_d + a.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = lane + i * TPR;
         if (!on || v >= nvec) continue;
-        float g[8], o[8];
+        if (!KEEP) load_param(a.pre_gamma, v, gpre);
+        float2 o[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = 1.0f;
-        if (a.pre_gamma) {
-          Vec8<float> t;
-          t.load(a.pre_gamma + 8 * v);
-          t.get(g);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = r[i][e] * inv * g[e];
+        for (int e = 0; e < 4; ++e) o[e] = mul2(mul2(r[i][e], make_float2(inv, inv)), gpre[e]);
         Vec8<T> t;
-        t.set(o);
+        t.set2(o);
         t.store(static_cast<T*>(a.n) + base + 8 * v);
       }
     }
-    if constexpr (TPR > 32) __syncthreads();  // part[] is free again
   }
 }
 

@@ -29,20 +29,9 @@ struct Vec8<__nv_bfloat16> {
   __device__ __forceinline__ void store(__nv_bfloat16* p) const {
     *reinterpret_cast<uint4*>(p) = raw;
   }
-  __device__ __forceinline__ void zero() { raw = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float f[8]) const {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 t = __bfloat1622float2(h[j]);
-      f[2 * j] = t.x;
-      f[2 * j + 1] = t.y;
-    }
-  }
-  __device__ __forceinline__ void set(const float f[8]) {
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+  __device__ __forceinline__ void set2(const float2 f[4]) {
+    raw = make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y),
+                     pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y));
   }
 };
 
@@ -63,14 +52,9 @@ struct Vec8<float> {
     reinterpret_cast<float4*>(p)[0] = a;
     reinterpret_cast<float4*>(p)[1] = b;
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float f[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
-  __device__ __forceinline__ void set(const float f[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void set2(const float2 f[4]) {
+    a = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    b = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
   }
 };
 

@@ -340,7 +340,7 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, const DeviceInfo* di, cuda
   auto go = [&](auto kernel, int tpr) {
     const int threads = tpr > 256 ? tpr : 256, rpb = threads / tpr;
     long long blocks = (a.rows + rpb - 1) / rpb;
-    const long long most = (long long)di->sms * (2048 / threads);
+    const long long most = (long long)di->sms * (threads > 256 ? 1 : 2);  // all resident
     if (blocks > most) blocks = most;
     return launch_pdl<true>(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
   };
