@@ -335,42 +335,62 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) 
 }
 
 // One token.  A block per (sequence, head): the state's N x P values as float4 columns, row
-// groups side by side, each thread walking its rows; the row groups' shares of the read meet in
-// shared memory.
+// groups side by side, each thread eight of its rows at a time, all on their way before the
+// first is used (with a load after each store the compiler must keep them in order, and two
+// loads a thread were in flight).  The row groups' shares of the read meet in shared memory.
+// Bound by the state's bytes, read and written once: 64 x 64 heads of 128 x 64.
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   __shared__ __align__(16) float part[256 * 4];
+  __shared__ float sk[256], sq[256];
   const int h = blockIdx.x % a.H, b = blockIdx.x / a.H, g = h / (a.H / a.G);
   const int cols = a.P / 4, groups = 256 / cols;
   const int c = threadIdx.x % cols, grp = threadIdx.x / cols;
-  const T* kp = static_cast<const T*>(a.k) + b * a.k_stride + (size_t)g * a.N;
-  const T* qp = static_cast<const T*>(a.q) + b * a.q_stride + (size_t)g * a.N;
   const T* vp = static_cast<const T*>(a.v) + b * a.v_stride + (size_t)h * a.P;
+  float4* Mp = reinterpret_cast<float4*>(a.M + ((size_t)b * a.H + h) * a.N * a.P) + c;
+  float4 m[8];
+  auto fetch = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = n0 + i * groups;
+      if (grp < groups && n < a.N) m[i] = __ldcs(Mp + (size_t)n * cols);
+    }
+  };
+  fetch(grp);
+  if (threadIdx.x < a.N) {
+    const size_t at = (size_t)g * a.N + threadIdx.x;
+    sk[threadIdx.x] = to_f32(static_cast<const T*>(a.k)[b * a.k_stride + at]);
+    sq[threadIdx.x] = to_f32(static_cast<const T*>(a.q)[b * a.q_stride + at]);
+  }
+  const float4 v4 = grp < groups ? load4_f32(vp + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
   const float d = ssm_step_size(
       to_f32(static_cast<const T*>(a.dt)[b * a.dt_stride + h]) + bias, a.softplus);
   const float al = expf(d * a.A[h]);
-  float4* Mp = reinterpret_cast<float4*>(a.M + ((size_t)b * a.H + h) * a.N * a.P);
+  const float dv[4] = {d * v4.x, d * v4.y, d * v4.z, d * v4.w};
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
   if (grp < groups) {
-    float dv[4];
+    for (int n0 = grp; n0 < a.N; n0 += 8 * groups) {
+      if (n0 != grp) fetch(n0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dv[i] = d * to_f32(vp[4 * c + i]);
-#pragma unroll 8
-    for (int n = grp; n < a.N; n += groups) {
-      float4 m = Mp[(size_t)n * cols + c];
-      const float kn = to_f32(kp[n]), qn = to_f32(qp[n]);
-      m.x = fmaf(m.x, al, dv[0] * kn);
-      m.y = fmaf(m.y, al, dv[1] * kn);
-      m.z = fmaf(m.z, al, dv[2] * kn);
-      m.w = fmaf(m.w, al, dv[3] * kn);
-      acc.x = fmaf(qn, m.x, acc.x);
-      acc.y = fmaf(qn, m.y, acc.y);
-      acc.z = fmaf(qn, m.z, acc.z);
-      acc.w = fmaf(qn, m.w, acc.w);
-      Mp[(size_t)n * cols + c] = m;
+      for (int i = 0; i < 8; ++i) {
+        const int n = n0 + i * groups;
+        if (n >= a.N) continue;
+        const float kn = sk[n], qn = sq[n];
+        float4 t;
+        t.x = fmaf(m[i].x, al, dv[0] * kn);
+        t.y = fmaf(m[i].y, al, dv[1] * kn);
+        t.z = fmaf(m[i].z, al, dv[2] * kn);
+        t.w = fmaf(m[i].w, al, dv[3] * kn);
+        acc.x = fmaf(qn, t.x, acc.x);
+        acc.y = fmaf(qn, t.y, acc.y);
+        acc.z = fmaf(qn, t.z, acc.z);
+        acc.w = fmaf(qn, t.w, acc.w);
+        __stcs(Mp + (size_t)n * cols, t);
+      }
     }
     *reinterpret_cast<float4*>(&part[(grp * cols + c) * 4]) = acc;
   }
