@@ -379,8 +379,8 @@ typedef struct {
 } sdm_ssm_shape;
 
 /* Bytes of scratch that sdm_ssm_forward needs for this shape on the calling device, packed or
- * not: the states between the segments of long sequences.  0 where it needs none (and for an
- * invalid shape, which the call refuses). */
+ * not: the decay sums of blocks of tokens, and the states between the segments of long
+ * sequences.  0 where it needs none (and for an invalid shape, which the call refuses). */
 size_t sdm_ssm_workspace_size(sdm_ssm_shape shape);
 
 /*

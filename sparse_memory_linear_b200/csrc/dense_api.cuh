@@ -225,7 +225,7 @@ struct SsmCost {
 struct SsmPlan {
   long long seg_rows, items;  // rows of a segment; (sequence, segment) pairs at most
   bool split;
-  size_t off_decays, bytes;
+  size_t off_decays, off_prep, bytes;
 };
 
 SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, const SsmCost& c) {
@@ -259,11 +259,17 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, c
 }
 
 SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
-  if (block)
-    return ssm_plan(s, packed, (long long)s.H * ((s.d_v + SB_P - 1) / SB_P),
-                    SsmCost{SB_L, sms, 3.5, 1.9, 12.0});
-  return ssm_plan(s, packed, (long long)s.H * ((s.d_v + SSM_COLS - 1) / SSM_COLS),
-                  SsmCost{16, 5 * sms, 1.6, 1.2, 12.0});
+  if (!block)
+    return ssm_plan(s, packed, (long long)s.H * ((s.d_v + SSM_COLS - 1) / SSM_COLS),
+                    SsmCost{16, 5 * sms, 1.6, 1.2, 12.0});
+  SsmPlan p = ssm_plan(s, packed, (long long)s.H * ((s.d_v + SB_P - 1) / SB_P),
+                       SsmCost{SB_L, sms, 3.3, 1.0, 12.0});
+  // every block's sums, where ssm_first_block puts them
+  const long long blocks = packed ? s.T / SB_L + s.B + 1
+                                  : s.B * (((long long)s.T + SB_L - 1) / SB_L);
+  p.off_prep = p.bytes;
+  p.bytes += round_up((size_t)blocks * s.H * sizeof(SsmPrep), WS_ALIGN);
+  return p;
 }
 
 SsmSplit ssm_split(const SsmPlan& plan, void* ws) {
@@ -315,6 +321,7 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
   SsmBlockArgs ba;
   ba.a = a;
   ba.sp = ssm_split(plan, ws);
+  ba.prep = reinterpret_cast<SsmPrep*>(static_cast<char*>(ws) + plan.off_prep);
   ba.ptiles = (s.d_v + SB_P - 1) / SB_P;
   if (!tile_map(&ba.mq, a.q, s.N, s.G, a.seq.R, a.q_stride) ||
       !tile_map(&ba.mk, a.k, s.N, s.G, a.seq.R, a.k_stride) ||
@@ -322,6 +329,11 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
     return SDM_ERR_CUDA;
   const long long blocks = plan.items * s.H * ba.ptiles;
   if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;
+  const long long preps = plan.items * (plan.seg_rows / SB_L);
+  if (preps > 2147483647LL) return SDM_ERR_UNSUPPORTED;
+  SDM_CUDA_TRY(launch_pdl<true>(ssm_prep_kernel, dim3((unsigned)preps, (unsigned)(s.H + 7) / 8),
+                                dim3(256), 0, st, a, ba.sp, ba.prep));
+  g_launches.fetch_add(1, std::memory_order_relaxed);
   if (plan.split) {
     SDM_CUDA_TRY(launch_pdl(ssm_segment_kernel, dim3((unsigned)blocks), dim3(SG_THREADS),
                             (size_t)SG_SMEM, st, ba));

@@ -20,8 +20,8 @@
 //   Y   a thread per token row: y = exp(c_t) Y2 + Y1 + D v, gated and stored
 //   H   a thread per state row: adds dM to the decayed state, publishes the state's two parts
 //   W   a thread per quarter row of v: w o v in parts, 32 tokens at a time
-//   and four single warps: step sizes and decay sums two blocks ahead; dM and Y1; Y2 and S;
-//   TMA loads of q and k (group Y loads v)
+//   and four single warps: dM and Y1; Y2 and S; loads of q and k (group Y loads v); loads of the
+//   blocks' sums
 // joined by mbarriers.  A block's work is a chain of short dependent steps; with the steps on
 // warps of their own the chains of successive blocks overlap.
 //
@@ -48,24 +48,27 @@ constexpr uint32_t SB_V = SB_K + 4 * SB_PANEL;             // 2 stages
 constexpr uint32_t SB_H = SB_V + 2 * SB_PANEL;             // two parts of the state
 constexpr uint32_t SB_W = SB_H + 2 * SB_PANEL;             // 2 quarters x 3 parts x 32 rows
 constexpr uint32_t SB_WPART = 4096;
-constexpr uint32_t SB_PREP = SB_W + 6 * SB_WPART;          // 2 x SsmPrep
+constexpr uint32_t SB_PREP = SB_W + 6 * SB_WPART;          // 4 x SsmPrep
+
+// What the kernels need of a block's step sizes (ssm_prep_kernel).
 struct SsmPrep {
   float d[SB_L];      // step size
   float in[SB_L];     // log2 decay from the run's start up to and with the token
   float out[SB_L];    // d * 2^(log2 decay after the token to the run's end)
   float w[SB_L];      // d * 2^(log2 decay after the token to the block's end)
   float run[4];       // log2 decay of each run
-  float pad[28];
+  float pad[28];      // a multiple of 128 bytes
 };
-constexpr uint32_t SB_BARS = SB_PREP + 2 * sizeof(SsmPrep);
+static_assert(sizeof(SsmPrep) == 2176, "a block's sums");
+constexpr uint32_t SB_BARS = SB_PREP + 4 * sizeof(SsmPrep);
 enum {
   BAR_QFULL = 0, BAR_QFREE = 2, BAR_KFULL = 4, BAR_KFREE = 6, BAR_VFULL = 8, BAR_VFREE = 10,
-  BAR_PREP = 12, BAR_PREPFREE = 14, BAR_WREADY = 16, BAR_WFREE = 18, BAR_YFREE = 20,
-  BAR_S = 22, BAR_P = 24, BAR_Y = 26, BAR_DM = 28, BAR_DMFREE = 30, BAR_Y2 = 32,
-  BAR_HREADY = 34, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 2
+  BAR_PREP = 12, BAR_PREPFREE = 16, BAR_WREADY = 20, BAR_WFREE = 22, BAR_YFREE = 24,
+  BAR_S = 26, BAR_P = 28, BAR_Y = 30, BAR_DM = 32, BAR_DMFREE = 34, BAR_Y2 = 36,
+  BAR_HREADY = 38, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 2
 };
-constexpr uint32_t SB_TMEM_PTR = SB_BARS + 40 * 8;
-static_assert(BAR_COUNT <= 40, "barriers");
+constexpr uint32_t SB_TMEM_PTR = SB_BARS + 44 * 8;
+static_assert(BAR_COUNT <= 44, "barriers");
 constexpr uint32_t SB_SMEM = SB_TMEM_PTR + 32 + 1024;      // and room to align
 static_assert(SB_SMEM <= 232448 - 64, "shared memory of a block");
 
@@ -79,8 +82,15 @@ struct SsmBlockArgs {
   SsmArgs a;
   CUtensorMap mq, mk, mv;
   SsmSplit sp;      // segments of whole blocks
+  SsmPrep* prep;    // [blocks, H]
   int ptiles;       // 64-column tiles of d_v
 };
+
+// The place of a sequence's first block among all blocks' sums: sequences of T rows one after
+// another, or for packed ones start / L + b, which leaves each room for ceil(length / L).
+__device__ __forceinline__ long long ssm_first_block(const SeqBounds& seq, int b) {
+  return seq.cu ? seq.start(b) / SB_L + b : (long long)b * ((seq.T + SB_L - 1) / SB_L);
+}
 
 // A block's step sizes and decay sums, by one warp: lane l holds tokens 4 l .. 4 l + 3.
 struct SsmSums {
@@ -125,6 +135,60 @@ __device__ __forceinline__ void ssm_sums(const float raw[4], const bool live[4],
   o.tail[1] = after + (la[2] + la[3]);
   o.tail[2] = after + la[3];
   o.tail[3] = after;
+}
+
+// Step sizes and decay sums of every block and head, once for all tiles and passes: a warp per
+// (block, head), a CTA's eight warps on neighbouring heads, whose dt share sectors.  Made inside
+// the scan by one warp a block this was a chain of 3000 cycles, most of a block's time.
+__global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, SsmPrep* prep) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  __shared__ int s_ok, s_b;
+  __shared__ long long s_seg;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y * 8 + warp;
+  const int seg_blocks = (int)(sp.seg_rows / SB_L);
+  const long long item = blockIdx.x / seg_blocks;
+  const int c = (int)(blockIdx.x % seg_blocks);
+  if (warp == 0) {
+    int b = 0;
+    long long seg = 0;
+    const bool ok = ssm_find_item(a.seq, item, sp.seg_rows, &b, &seg);
+    if (lane == 0) {
+      s_ok = ok;
+      s_b = b;
+      s_seg = seg;
+    }
+  }
+  __syncthreads();
+  if (!s_ok || h >= a.H) return;
+  const long long seq0 = a.seq.start(s_b), seq1 = a.seq.end(s_b);
+  const long long row0 = seq0 + s_seg * sp.seg_rows + (long long)c * SB_L;
+  if (row0 >= seq1) return;
+  const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
+  const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+  float raw[4];
+  bool live[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long r = row0 + 4 * lane + i;
+    live[i] = r < seq1;
+    raw[i] = live[i] ? __bfloat162float(dp[r * a.dt_stride]) : 0.0f;
+  }
+  SsmSums o;
+  ssm_sums(raw, live, bias, A2, a.softplus, o);
+  float out[4], w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[i] = o.d[i] * exp2f(o.tail[i]);
+    w[i] = o.d[i] * exp2f(o.tail[i] + o.later);
+  }
+  SsmPrep* pr = prep + (ssm_first_block(a.seq, s_b) + (row0 - seq0) / SB_L) * a.H + h;
+  reinterpret_cast<float4*>(pr->d)[lane] = make_float4(o.d[0], o.d[1], o.d[2], o.d[3]);
+  reinterpret_cast<float4*>(pr->in)[lane] = make_float4(o.in[0], o.in[1], o.in[2], o.in[3]);
+  reinterpret_cast<float4*>(pr->out)[lane] = make_float4(out[0], out[1], out[2], out[3]);
+  reinterpret_cast<float4*>(pr->w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
+  if (lane < 4)
+    pr->run[lane] = lane == 0 ? o.run[0] : lane == 1 ? o.run[1] : lane == 2 ? o.run[2] : o.run[3];
 }
 
 // Eight pairs of values times w, in three bf16 parts.
@@ -210,8 +274,6 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       mbar_init(bar(BAR_KFREE + i), 2);
       mbar_init(bar(BAR_VFULL + i), 1);
       mbar_init(bar(BAR_VFREE + i), 4);
-      mbar_init(bar(BAR_PREP + i), 1);
-      mbar_init(bar(BAR_PREPFREE + i), 16);
       mbar_init(bar(BAR_WREADY + i), 4);
       mbar_init(bar(BAR_WFREE + i), 1);
       mbar_init(bar(BAR_S + i), 1);
@@ -221,6 +283,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       mbar_init(bar(BAR_YFREE + i), 4);
       mbar_init(bar(BAR_DM + i), 1);
       mbar_init(bar(BAR_DMFREE + i), 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(BAR_PREP + i), 1);
+      mbar_init(bar(BAR_PREPFREE + i), 16);
     }
     mbar_init(bar(BAR_HREADY), 4);
     mbar_init(bar(BAR_HFREE), 1);
@@ -243,7 +309,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   // phase of the c-th use of a barrier that completes once per block, or per two of them
   auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u, abort); };
   auto prep = [&](int c) {
-    return reinterpret_cast<SsmPrep*>(sm + SB_PREP + (c & 1) * sizeof(SsmPrep));
+    return reinterpret_cast<SsmPrep*>(sm + SB_PREP + (c & 3) * sizeof(SsmPrep));
   };
 
   if (warp < 4) {
@@ -252,7 +318,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     for (int c = 0; c < nb; ++c) {
       const uint32_t stage = c & 1;
-      if (!wait(BAR_PREP + stage, c >> 1) || !wait(BAR_S + stage, c >> 1)) break;
+      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_S + stage, c >> 1)) break;
       tc_fence_after();
       const SsmPrep& pr = *prep(c);
       const uint32_t sbuf = tm + TM_S + stage * 128 + lanes;
@@ -322,7 +388,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(BAR_P + stage));
-        mbar_arrive(bar(BAR_PREPFREE + stage));
+        mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
       }
     }
   } else if (warp < 8) {
@@ -355,7 +421,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       const bool live = row < row1;
       const __nv_bfloat16* const zrow = zp + row * a.gate_stride;
       __nv_bfloat16* const yrow = yp + (size_t)row * a.H * a.P;
-      if (!wait(BAR_PREP + stage, c >> 1) || !wait(BAR_VFULL + stage, c >> 1)) break;
+      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_VFULL + stage, c >> 1)) break;
       float decay;  // from the block's start up to t
       {
         const SsmPrep& pr = *prep(c);
@@ -367,7 +433,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
       const float2 f2 = make_float2(decay, decay);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + stage));
+      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
       uint32_t z[8];
       auto load_z = [&](int part) {
         if (!zp || !live || 16 * part >= pn) return;
@@ -484,12 +550,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     published();
     bool ok = true;
     for (int c = 0; c < nb; ++c) {
-      ok = wait(BAR_PREP + (c & 1), c >> 1);
+      ok = wait(BAR_PREP + (c & 3), c >> 2);
       if (!ok) break;
       const SsmPrep& pr = *prep(c);
       const float keep = exp2f((pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]));
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 1)));
+      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
       ok = wait(BAR_DM + (c & 1), c >> 1);
       if (!ok) break;
       tc_fence_after();
@@ -529,7 +595,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
     for (int c = 0; c < nb; ++c) {
       const int stage = c & 1;
-      if (!wait(BAR_PREP + stage, c >> 1) || !wait(BAR_VFULL + stage, c >> 1)) break;
+      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_VFULL + stage, c >> 1)) break;
       uint8_t* vtile = sm + SB_V + stage * SB_PANEL;
       const float* w = prep(c)->w;
       const long long left = row1 - (row0 + (long long)c * SB_L);
@@ -563,7 +629,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (lane == 0) mbar_arrive(bar(BAR_WREADY + buf));
       }
       if (!ok) break;
-      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + stage));
+      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
     }
   } else if (warp >= 16) {
   if (warp == 18) {
@@ -689,44 +755,23 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
     }
   } else {
-    // ------------------------------------------------ step sizes and decay sums
-    const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
-    const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-    float raw[4];
-    auto row_of = [&](int c, int i) { return row0 + (long long)c * SB_L + 4 * lane + i; };
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        raw[i] = row_of(c, i) < row1 ? __bfloat162float(dp[row_of(c, i) * a.dt_stride]) : 0.0f;
-    };
-    fetch(0);
-    auto prepare = [&](int c) -> bool {
-      SsmSums o;
-      bool live[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) live[i] = row_of(c, i) < row1;
-      ssm_sums(raw, live, bias, A2, a.softplus, o);
-      if (c + 1 < nb) fetch(c + 1);
-      float out[4], w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        out[i] = o.d[i] * exp2f(o.tail[i]);
-        w[i] = o.d[i] * exp2f(o.tail[i] + o.later);
+    // ------------------------------------------------ loads of the blocks' sums
+    if (lane == 0) {
+      const SsmPrep* from =
+          ba.prep + (ssm_first_block(a.seq, b) + (row0 - seq0) / SB_L) * a.H + h;
+      int n = 0;
+      for (int c = 0; c < nb; ++c) {
+        const uint32_t slot = c & 3;
+        if (c >= 4 && !wait(BAR_PREPFREE + slot, (c >> 2) - 1)) break;
+        mbar_expect(bar(BAR_PREP + slot), sizeof(SsmPrep));
+        bulk_load(base + SB_PREP + slot * sizeof(SsmPrep), from + (size_t)c * a.H,
+                  sizeof(SsmPrep), bar(BAR_PREP + slot));
+        n = c + 1;
       }
-      if (c >= 2 && !wait(BAR_PREPFREE + (c & 1), (c >> 1) - 1)) return false;
-      SsmPrep* pr = prep(c);
-      reinterpret_cast<float4*>(pr->d)[lane] = make_float4(o.d[0], o.d[1], o.d[2], o.d[3]);
-      reinterpret_cast<float4*>(pr->in)[lane] = make_float4(o.in[0], o.in[1], o.in[2], o.in[3]);
-      reinterpret_cast<float4*>(pr->out)[lane] = make_float4(out[0], out[1], out[2], out[3]);
-      reinterpret_cast<float4*>(pr->w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
-      if (lane < 4)
-        pr->run[lane] = lane == 0 ? o.run[0] : lane == 1 ? o.run[1] : lane == 2 ? o.run[2] : o.run[3];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_PREP + (c & 1)));
-      return true;
-    };
-    for (int c = 0; c < nb; ++c)
-      if (!prepare(c)) break;
+      if (*abort)
+        for (int c = n > 4 ? n - 4 : 0; c < n; ++c)
+          mbar_wait(bar(BAR_PREP + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
+    }
   }
   }
   tc_fence_before();
@@ -743,16 +788,16 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 // weight, its decay up to the segment's end, is known when its block is read, and all blocks
 // accumulate in the same tensor memory.
 //   warps 0-7  w o v in parts, two groups at alternate quarters
-//   warp 8 products, warp 9 loads, warp 10 step sizes and decay sums
-constexpr int SG_THREADS = 384;
-constexpr uint32_t SG_K = 0;                        // 2 stages x 2 panels
-constexpr uint32_t SG_V = SG_K + 4 * SB_PANEL;      // 2 stages
-constexpr uint32_t SG_W = SG_V + 2 * SB_PANEL;      // 4 quarters x 3 parts
-constexpr uint32_t SG_WT = SG_W + 12 * SB_WPART;    // 2 x 128 weights
-constexpr uint32_t SG_BARS = SG_WT + 2 * SB_L * 4;
-enum { GB_KVFULL = 0, GB_KVFREE = 2, GB_PREP = 4, GB_PREPFREE = 6, GB_WREADY = 8, GB_WFREE = 12,
-       GB_DONE = 16, GB_COUNT };
-constexpr uint32_t SG_TMEM_PTR = SG_BARS + 20 * 8;
+//   warp 8 products, warp 9 loads
+constexpr int SG_THREADS = 320;
+constexpr int SG_STAGES = 3;
+constexpr uint32_t SG_K = 0;                                // stages x 2 panels
+constexpr uint32_t SG_V = SG_K + SG_STAGES * 2 * SB_PANEL;  // stages
+constexpr uint32_t SG_W = SG_V + SG_STAGES * SB_PANEL;      // 4 quarters x 3 parts
+constexpr uint32_t SG_PREP = SG_W + 12 * SB_WPART;          // stages x SsmPrep
+constexpr uint32_t SG_BARS = SG_PREP + SG_STAGES * sizeof(SsmPrep);
+enum { GB_FULL = 0, GB_FREE = 3, GB_WREADY = 6, GB_WFREE = 10, GB_DONE = 14, GB_COUNT };
+constexpr uint32_t SG_TMEM_PTR = SG_BARS + 16 * 8;
 constexpr uint32_t SG_SMEM = SG_TMEM_PTR + 32 + 1024;
 
 __global__ void __launch_bounds__(SG_THREADS, 1)
@@ -792,11 +837,9 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
 
   if (warp == 0) tmem_alloc(base + SG_TMEM_PTR, 128);
   if (tid == 32) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(GB_KVFULL + i), 1);
-      mbar_init(bar(GB_KVFREE + i), 1);
-      mbar_init(bar(GB_PREP + i), 1);
-      mbar_init(bar(GB_PREPFREE + i), 8);
+    for (int i = 0; i < SG_STAGES; ++i) {
+      mbar_init(bar(GB_FULL + i), 1);
+      mbar_init(bar(GB_FREE + i), 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(GB_WREADY + i), 4);
@@ -807,7 +850,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
   }
   if (npanels == 1) {
     uint4* z = reinterpret_cast<uint4*>(sm + SG_K);
-    for (int i = tid; i < 2 * (int)SB_PANEL / 16; i += SG_THREADS) {
+    for (int i = tid; i < SG_STAGES * (int)SB_PANEL / 16; i += SG_THREADS) {
       const int stage = i / (SB_PANEL / 16), j = i % (SB_PANEL / 16);
       z[(2 * stage + 1) * (SB_PANEL / 16) + j] = make_uint4(0, 0, 0, 0);
     }
@@ -819,32 +862,41 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + SG_TMEM_PTR);
   volatile int* const abort = &s_abort;
   auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u, abort); };
-  float* const weights = reinterpret_cast<float*>(sm + SG_WT);
+  auto prep = [&](int stage) {
+    return reinterpret_cast<const SsmPrep*>(sm + SG_PREP + stage * sizeof(SsmPrep));
+  };
 
   if (warp < 8) {
     const int grp = warp >> 2, i0 = tid & 127, rq = i0 >> 2;
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
     bool ok = true;
-    for (int c = 0; c < nb && ok; ++c) {
-      const int stage = c & 1;
-      ok = wait(GB_PREP + stage, c >> 1) && wait(GB_KVFULL + stage, c >> 1);
+    float carry = 0.0f;  // log2 decay of the blocks behind
+    for (int c = 0, stage = 0, round = 0; c < nb && ok; ++c) {
+      ok = wait(GB_FULL + stage, round);
       if (!ok) break;
       const uint8_t* vtile = sm + SG_V + stage * SB_PANEL;
+      const SsmPrep& pr = *prep(stage);
+      const float f = exp2f(carry);
+      carry += (pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int qd = 2 * i + grp;  // the group's buffers: qd
         uint32_t p[3][8];
         ssm_parts(*reinterpret_cast<const uint4*>(vtile + 4096 * qd + o0),
                   *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o1),
-                  weights[stage * SB_L + 32 * qd + rq], p);
+                  pr.w[32 * qd + rq] * f, p);
         ok = ok && (c == 0 || wait(GB_WFREE + qd, c - 1));
         ssm_store_parts(sm + SG_W + qd * 3 * SB_WPART, o0, o1, p);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(GB_WREADY + qd));
       }
-      if (lane == 0) mbar_arrive(bar(GB_PREPFREE + stage));
+      if (++stage == SG_STAGES) {
+        stage = 0;
+        ++round;
+      }
     }
+    if (tid == 0 && p0 == 0) ba.sp.decays[item * a.H + h] = exp2f(carry);
     if (warp < 4 && ok && wait(GB_DONE, 0)) {
       tc_fence_after();
       const int n = tid, pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;
@@ -869,11 +921,10 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
     constexpr uint32_t dM = mma_desc(128, 128, 1, 1), dM2 = mma_desc(128, 64, 1, 1);
     const uint32_t k0 = tile_desc(base + SG_K, SB_PANEL), w0 = tile_desc(base + SG_W, SB_WPART);
     bool ok = true;
-    for (int c = 0; c < nb && ok; ++c) {
-      const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
-      ok = wait(GB_KVFULL + stage, c >> 1);
+    for (int c = 0, stage = 0; c < nb && ok; ++c) {
+      const uint32_t k = k0 + stage * (2 * SB_PANEL >> 4);
       for (int qd = 0; qd < 4 && ok; ++qd) {
-        ok = wait(GB_WREADY + qd, c);
+        ok = wait(GB_WREADY + qd, c);  // the block's tiles are there: its weights were made
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -884,60 +935,40 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
             mma_ss(tm, kq + i * (2048 >> 4), w + ((2 * SB_WPART + i * 2048) >> 4), dM2, true);
           }
           mma_commit(bar(GB_WFREE + qd));
-          if (qd == 3) mma_commit(bar(GB_KVFREE + stage));
+          if (qd == 3) mma_commit(bar(GB_FREE + stage));
         }
         __syncwarp();
       }
+      if (++stage == SG_STAGES) stage = 0;
     }
     if (elect_one()) mma_commit(bar(GB_DONE));
     __syncwarp();
     mbar_wait(bar(GB_DONE), 0, abort);
-  } else if (warp == 9) {
+  } else {
     if (lane == 0) {
-      int c = 0;
-      for (; c < nb; ++c) {
-        const uint32_t stage = c & 1;
-        const int r = (int)(row0 + (long long)(nb - 1 - c) * SB_L);
-        if (c >= 2 && !wait(GB_KVFREE + stage, (c >> 1) - 1)) break;
-        mbar_expect(bar(GB_KVFULL + stage), (npanels + 1) * SB_PANEL);
-        tma_load_3d(base + SG_V + stage * SB_PANEL, &ba.mv, p0, h, r, bar(GB_KVFULL + stage));
+      const SsmPrep* from = ba.prep +
+          (ssm_first_block(a.seq, s_b) + (row0 - a.seq.start(s_b)) / SB_L) * a.H + h;
+      int n = 0;
+      for (int c = 0, stage = 0, round = 0; c < nb; ++c) {
+        const int at = nb - 1 - c, r = (int)(row0 + (long long)at * SB_L);
+        if (c >= SG_STAGES && !wait(GB_FREE + stage, round - 1)) break;
+        mbar_expect(bar(GB_FULL + stage), (npanels + 1) * SB_PANEL + sizeof(SsmPrep));
+        bulk_load(base + SG_PREP + stage * sizeof(SsmPrep), from + (size_t)at * a.H,
+                  sizeof(SsmPrep), bar(GB_FULL + stage));
+        tma_load_3d(base + SG_V + stage * SB_PANEL, &ba.mv, p0, h, r, bar(GB_FULL + stage));
         for (int pl = 0; pl < npanels; ++pl)
           tma_load_3d(base + SG_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
-                      bar(GB_KVFULL + stage));
+                      bar(GB_FULL + stage));
+        n = c + 1;
+        if (++stage == SG_STAGES) {
+          stage = 0;
+          ++round;
+        }
       }
-      if (*abort) {
-        int none = 0;
-        for (int e = c > 2 ? c - 2 : 0; e < c; ++e)
-          mbar_wait(bar(GB_KVFULL + (e & 1)), (uint32_t)(e >> 1) & 1u, &none);
-      }
+      if (*abort)
+        for (int c = n > SG_STAGES ? n - SG_STAGES : 0; c < n; ++c)
+          mbar_wait(bar(GB_FULL + c % SG_STAGES), (uint32_t)(c / SG_STAGES) & 1u, abort);
     }
-  } else if (warp == 10) {
-    const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
-    const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-    float raw[4], carry = 0.0f;  // log2 decay of the blocks behind
-    const bool live[4] = {true, true, true, true};
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        raw[i] = __bfloat162float(
-            dp[(row0 + (long long)(nb - 1 - c) * SB_L + 4 * lane + i) * a.dt_stride]);
-    };
-    fetch(0);
-    for (int c = 0; c < nb; ++c) {
-      SsmSums o;
-      ssm_sums(raw, live, bias, A2, a.softplus, o);
-      if (c + 1 < nb) fetch(c + 1);
-      float w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = o.d[i] * exp2f((o.tail[i] + o.later) + carry);
-      carry += (o.run[0] + o.run[1]) + (o.run[2] + o.run[3]);
-      if (c >= 2 && !wait(GB_PREPFREE + (c & 1), (c >> 1) - 1)) break;
-      reinterpret_cast<float4*>(weights + (c & 1) * SB_L)[lane] =
-          make_float4(w[0], w[1], w[2], w[3]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(GB_PREP + (c & 1)));
-    }
-    if (lane == 0 && p0 == 0) ba.sp.decays[item * a.H + h] = exp2f(carry);
   }
   tc_fence_before();
   __syncthreads();
