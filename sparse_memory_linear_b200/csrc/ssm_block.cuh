@@ -20,8 +20,8 @@
 //   Y   a thread per token row: y = exp(c_t) Y2 + Y1 + D v, gated and stored
 //   H   a thread per state row: adds dM to the decayed state, publishes the state's two parts
 //   W   a thread per quarter row of v: w o v in parts, 32 tokens at a time
-//   and four single warps: dM and Y1; Y2 and S; loads of q and k (group Y loads v); loads of the
-//   blocks' sums
+//   and four single warps: dM and Y1; Y2 and S; loads of q and k; loads of v and of the blocks'
+//   sums
 // joined by mbarriers.  A block's work is a chain of short dependent steps; with the steps on
 // warps of their own the chains of successive blocks overlap.
 //
@@ -42,10 +42,10 @@ constexpr int SB_THREADS = 640;
 
 // Shared memory, from a 1024-byte boundary.
 constexpr uint32_t SB_PANEL = 16384;                       // 128 rows of 128 bytes
-constexpr uint32_t SB_Q = 0;                               // 2 stages x 2 panels
-constexpr uint32_t SB_K = SB_Q + 4 * SB_PANEL;             // 2 stages x 2 panels
-constexpr uint32_t SB_V = SB_K + 4 * SB_PANEL;             // 2 stages
-constexpr uint32_t SB_H = SB_V + 2 * SB_PANEL;             // two parts of the state
+constexpr uint32_t SB_Q = 0;                               // 2 panels
+constexpr uint32_t SB_K = SB_Q + 2 * SB_PANEL;             // 2 stages x 2 panels
+constexpr uint32_t SB_V = SB_K + 4 * SB_PANEL;             // 4 stages
+constexpr uint32_t SB_H = SB_V + 4 * SB_PANEL;             // two parts of the state
 constexpr uint32_t SB_W = SB_H + 2 * SB_PANEL;             // 2 quarters x 3 parts x 32 rows
 constexpr uint32_t SB_WPART = 4096;
 constexpr uint32_t SB_PREP = SB_W + 6 * SB_WPART;          // 4 x SsmPrep
@@ -62,10 +62,10 @@ struct SsmPrep {
 static_assert(sizeof(SsmPrep) == 2176, "a block's sums");
 constexpr uint32_t SB_BARS = SB_PREP + 4 * sizeof(SsmPrep);
 enum {
-  BAR_QFULL = 0, BAR_QFREE = 2, BAR_KFULL = 4, BAR_KFREE = 6, BAR_VFULL = 8, BAR_VFREE = 10,
-  BAR_PREP = 12, BAR_PREPFREE = 16, BAR_WREADY = 20, BAR_WFREE = 22, BAR_YFREE = 24,
-  BAR_S = 26, BAR_P = 28, BAR_Y = 30, BAR_DM = 32, BAR_DMFREE = 34, BAR_Y2 = 36,
-  BAR_HREADY = 38, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 2
+  BAR_QFULL = 0, BAR_QFREE, BAR_KFULL = 2, BAR_KFREE = 4, BAR_VFULL = 6, BAR_VFREE = 10,
+  BAR_PREP = 14, BAR_PREPFREE = 18, BAR_WREADY = 22, BAR_WFREE = 24, BAR_YFREE = 26,
+  BAR_S = 28, BAR_P = 30, BAR_Y = 32, BAR_DM = 34, BAR_DMFREE = 36, BAR_Y2 = 38,
+  BAR_HREADY = 40, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 2
 };
 constexpr uint32_t SB_TMEM_PTR = SB_BARS + 44 * 8;
 static_assert(BAR_COUNT <= 44, "barriers");
@@ -268,12 +268,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   if (warp == 0) tmem_alloc(base + SB_TMEM_PTR, 512);
   if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(BAR_QFULL + i), 1);
-      mbar_init(bar(BAR_QFREE + i), 1);
       mbar_init(bar(BAR_KFULL + i), 1);
       mbar_init(bar(BAR_KFREE + i), 2);
-      mbar_init(bar(BAR_VFULL + i), 1);
-      mbar_init(bar(BAR_VFREE + i), 4);
       mbar_init(bar(BAR_WREADY + i), 4);
       mbar_init(bar(BAR_WFREE + i), 1);
       mbar_init(bar(BAR_S + i), 1);
@@ -287,7 +283,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(BAR_PREP + i), 1);
       mbar_init(bar(BAR_PREPFREE + i), 16);
+      mbar_init(bar(BAR_VFULL + i), 1);
+      mbar_init(bar(BAR_VFREE + i), 4);
     }
+    mbar_init(bar(BAR_QFULL), 1);
+    mbar_init(bar(BAR_QFREE), 1);
     mbar_init(bar(BAR_HREADY), 4);
     mbar_init(bar(BAR_HFREE), 1);
     for (int i = 0; i < 2; ++i) mbar_init(bar(BAR_DRAIN + i), 1);
@@ -333,18 +333,25 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           e += pr.run[j];
         }
       }
+      // 16 columns at a time, the next 16 on their way from tensor memory; the row's warp needs
+      // the runs up to its own
+      const int groups = 2 * warp + 2;
+      float next[16];
+      tmem_ld16(sbuf, next);
 #pragma unroll 1
-      for (int j = 0; j < 4; ++j) {  // runs of 32 columns
-        uint32_t pk[16];
-        if (j < warp) {
-          float s[32];
-          tmem_ld32(sbuf + 32 * j, s);
-          const float f = j == 0 ? to[0] : j == 1 ? to[1] : to[2];
-          const float2 f2 = make_float2(f, f);
-          const float4* o4 = reinterpret_cast<const float4*>(&pr.out[32 * j]);
-          tmem_wait_ld();
+      for (int grp = 0; grp < groups; ++grp) {
+        float s[16];
+        tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) s[i] = next[i];
+        if (grp + 1 < groups) tmem_ld16(sbuf + 16 * (grp + 1), next);
+        uint32_t pk[8];
+        if (grp < 2 * warp) {
+          const float f = grp < 2 ? to[0] : grp < 4 ? to[1] : to[2];
+          const float2 f2 = make_float2(f, f);
+          const float4* o4 = reinterpret_cast<const float4*>(&pr.out[16 * grp]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             const float4 o = o4[i];
             const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
                                   make_float2(s[4 * i], s[4 * i + 1]));
@@ -353,15 +360,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             pk[2 * i] = pack_bf16(u.x, u.y);
             pk[2 * i + 1] = pack_bf16(v.x, v.y);
           }
-        } else if (j == warp) {
-          float s[32];
-          tmem_ld32(sbuf + 32 * j, s);
-          const float4* in4 = reinterpret_cast<const float4*>(&pr.in[32 * j]);
-          const float4* d4 = reinterpret_cast<const float4*>(&pr.d[32 * j]);
+        } else {
+          const float4* in4 = reinterpret_cast<const float4*>(&pr.in[16 * grp]);
+          const float4* d4 = reinterpret_cast<const float4*>(&pr.d[16 * grp]);
           const float2 t2 = make_float2(in_t, in_t);
-          tmem_wait_ld();
+          const int own = t - 16 * grp;  // the row's own column among these
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             const float4 in = in4[i], d = d4[i];
             const float2 e0 = sub2(t2, make_float2(in.x, in.y)),
                          e1 = sub2(t2, make_float2(in.z, in.w));
@@ -369,19 +374,20 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                             make_float2(fast_exp2(e0.x), fast_exp2(e0.y)));
             float2 v = mul2(mul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(d.z, d.w)),
                             make_float2(fast_exp2(e1.x), fast_exp2(e1.y)));
-            if (4 * i > lane) u.x = 0.0f;
-            if (4 * i + 1 > lane) u.y = 0.0f;
-            if (4 * i + 2 > lane) v.x = 0.0f;
-            if (4 * i + 3 > lane) v.y = 0.0f;
+            if (4 * i > own) u.x = 0.0f;
+            if (4 * i + 1 > own) u.y = 0.0f;
+            if (4 * i + 2 > own) v.x = 0.0f;
+            if (4 * i + 3 > own) v.y = 0.0f;
             pk[2 * i] = pack_bf16(u.x, u.y);
             pk[2 * i + 1] = pack_bf16(v.x, v.y);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = 0u;
         }
-        // P's columns 16 j .. lie in columns of S that are already read
-        tmem_st16(sbuf + 16 * j, pk);
+        // P's columns 8 grp .. lie in columns of S that are already read
+        tmem_st8(sbuf + 8 * grp, pk);
+      }
+      {
+        const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int grp = groups; grp < 8; ++grp) tmem_st8(sbuf + 8 * grp, none);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -402,17 +408,6 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const __nv_bfloat16* const zp =
         a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)h * a.P + p0 : nullptr;
     // whole sectors where rows start on them and hold a multiple of 16 values
-    // the group that reads a tile of v last also loads the next one into its place
-    auto load_v = [&](int c) {
-      mbar_expect(bar(BAR_VFULL + (c & 1)), SB_PANEL);
-      tma_load_3d(base + SB_V + (c & 1) * SB_PANEL, &ba.mv, p0, h, (int)(row0 + (long long)c * SB_L),
-                  bar(BAR_VFULL + (c & 1)));
-    };
-    int loaded = nb < 2 ? nb : 2;
-    if (warp == 4 && lane == 0) {
-      load_v(0);
-      if (nb > 1) load_v(1);
-    }
     const bool sectors = a.P % 16 == 0 && a.gate_stride % 16 == 0 &&
                          ((reinterpret_cast<uintptr_t>(yp) | reinterpret_cast<uintptr_t>(zp)) & 31) == 0;
     for (int c = 0; c < nb; ++c) {
@@ -421,7 +416,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       const bool live = row < row1;
       const __nv_bfloat16* const zrow = zp + row * a.gate_stride;
       __nv_bfloat16* const yrow = yp + (size_t)row * a.H * a.P;
-      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_VFULL + stage, c >> 1)) break;
+      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_VFULL + (c & 3), c >> 2)) break;
       float decay;  // from the block's start up to t
       {
         const SsmPrep& pr = *prep(c);
@@ -449,7 +444,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       load_z(0);  // on its way while the products finish
       if (!wait(BAR_Y2 + stage, c >> 1) || !wait(BAR_Y + stage, c >> 1)) break;
       tc_fence_after();
-      const uint8_t* vtile = sm + SB_V + stage * SB_PANEL;
+      const uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
       const uint32_t ybuf = tm + TM_S + stage * 128 + TM_Y1 + lanes, y2buf = tm + TM_Y2 + stage * 64 + lanes;
 #pragma unroll 1
       for (int part = 0; part < 4; ++part) {
@@ -493,20 +488,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(BAR_YFREE + stage));
-        mbar_arrive(bar(BAR_VFREE + stage));
-        if (warp == 4 && c + 2 < nb && wait(BAR_VFREE + stage, c >> 1)) {
-          load_v(c + 2);
-          loaded = c + 3;
-          // a load from memory takes longer than a block's work: the one after that into L2
-          if (c + 4 < nb)
-            tma_prefetch_3d(&ba.mv, p0, h, (int)(row0 + (long long)(c + 4) * SB_L));
-        }
+        mbar_arrive(bar(BAR_VFREE + (c & 3)));
       }
-      __syncwarp();
     }
-    if (*abort && warp == 4 && lane == 0)
-      for (int c = loaded > 2 ? loaded - 2 : 0; c < loaded; ++c)
-        mbar_wait(bar(BAR_VFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
   } else if (warp < 12) {
     // ------------------------------------------------ H: row n = tid - 256
     const int n = tid - 256;
@@ -595,8 +579,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
     for (int c = 0; c < nb; ++c) {
       const int stage = c & 1;
-      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_VFULL + stage, c >> 1)) break;
-      uint8_t* vtile = sm + SB_V + stage * SB_PANEL;
+      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_VFULL + (c & 3), c >> 2)) break;
+      uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
       const float* w = prep(c)->w;
       const long long left = row1 - (row0 + (long long)c * SB_L);
       if (left < SB_L) {
@@ -614,13 +598,19 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         }
       }
       bool ok = true;
+      uint4 na = *reinterpret_cast<const uint4*>(vtile + o0),
+            nb4 = *reinterpret_cast<const uint4*>(vtile + o1);
+      float nw = w[rq];
 #pragma unroll 1
       for (int qd = 0; qd < 4; ++qd) {
         const int use = 4 * c + qd, buf = qd & 1;
-        const uint4 va = *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o0),
-                    vb = *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o1);
         uint32_t p[3][8];
-        ssm_parts(va, vb, w[32 * qd + rq], p);
+        ssm_parts(na, nb4, nw, p);
+        if (qd < 3) {
+          na = *reinterpret_cast<const uint4*>(vtile + 4096 * (qd + 1) + o0);
+          nb4 = *reinterpret_cast<const uint4*>(vtile + 4096 * (qd + 1) + o1);
+          nw = w[32 * (qd + 1) + rq];
+        }
         ok = use < 2 || wait(BAR_WFREE + buf, (use >> 1) - 1);
         if (!ok) break;
         ssm_store_parts(sm + SB_W + buf * 3 * SB_WPART, o0, o1, p);
@@ -644,33 +634,32 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (!wait(BAR_HREADY, c)) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t q = q0 + stage * (2 * SB_PANEL >> 4);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const uint32_t o = ((i >> 2 & 1) * SB_PANEL + (i & 3) * 32) >> 4;
             if ((i & 7) < nk)
-              mma_ss(tm + TM_Y2 + stage * 64, q + o,
+              mma_ss(tm + TM_Y2 + stage * 64, q0 + o,
                      h0 + (((i >> 3) * SB_PANEL + (i & 7) * 2048) >> 4), dY2, i > 0);
           }
           mma_commit(bar(BAR_Y2 + stage));
           mma_commit(bar(BAR_HFREE));
-          mma_commit(bar(BAR_QFREE + stage));
+          mma_commit(bar(BAR_QFREE));
         }
         __syncwarp();
       }
       const int e = c + 1;
       if (e < nb) {
         const uint32_t stage = e & 1;
-        if (!wait(BAR_QFULL + stage, e >> 1) || !wait(BAR_KFULL + stage, e >> 1) ||
+        if (!wait(BAR_QFULL, e) || !wait(BAR_KFULL + stage, e >> 1) ||
             (e >= 2 && !wait(BAR_YFREE + stage, (e >> 1) - 1)))
           break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t q = q0 + stage * (2 * SB_PANEL >> 4), k = k0 + stage * (2 * SB_PANEL >> 4);
+          const uint32_t k = k0 + stage * (2 * SB_PANEL >> 4);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t o = ((i >> 2) * SB_PANEL + (i & 3) * 32) >> 4;
-            if (i < nk) mma_ss(tm + TM_S + stage * 128, q + o, k + o, dS, i > 0);
+            if (i < nk) mma_ss(tm + TM_S + stage * 128, q0 + o, k + o, dS, i > 0);
           }
           mma_commit(bar(BAR_S + stage));
           mma_commit(bar(BAR_KFREE + stage));
@@ -711,11 +700,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         __syncwarp();
       }
       // the last quarter is also the sign that v's rows behind the end are zeros
-      ok = ok && wait(BAR_VFULL + stage, c >> 1) && wait(BAR_P + stage, c >> 1);
+      ok = ok && wait(BAR_VFULL + (c & 3), c >> 2) && wait(BAR_P + stage, c >> 1);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t v = v0 + stage * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
+        const uint32_t v = v0 + (c & 3) * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
 #pragma unroll
         for (int i = 0; i < SB_L / 16; ++i)
           mma_ts(s + TM_Y1, s + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
@@ -733,44 +722,51 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       for (int c = 0; c < nb; ++c) {
         const uint32_t stage = c & 1;
         const int r = (int)(row0 + (long long)c * SB_L);
-        if (c >= 2 && !wait(BAR_QFREE + stage, (c >> 1) - 1)) break;
-        mbar_expect(bar(BAR_QFULL + stage), npanels * SB_PANEL);
-        for (int pl = 0; pl < npanels; ++pl)
-          tma_load_3d(base + SB_Q + (2 * stage + pl) * SB_PANEL, &ba.mq, 64 * pl, g, r,
-                      bar(BAR_QFULL + stage));
-        qc = c + 1;
         if (c >= 2 && !wait(BAR_KFREE + stage, (c >> 1) - 1)) break;
         mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
         for (int pl = 0; pl < npanels; ++pl)
           tma_load_3d(base + SB_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
                       bar(BAR_KFULL + stage));
         kc = c + 1;
+        if (c >= 1 && !wait(BAR_QFREE, c - 1)) break;
+        mbar_expect(bar(BAR_QFULL), npanels * SB_PANEL);
+        for (int pl = 0; pl < npanels; ++pl)
+          tma_load_3d(base + SB_Q + pl * SB_PANEL, &ba.mq, 64 * pl, g, r, bar(BAR_QFULL));
+        qc = c + 1;
       }
       if (*abort) {
         // loads in flight land before the block's memory is given up (each wait limited)
-        for (int c = qc > 2 ? qc - 2 : 0; c < qc; ++c)
-          mbar_wait(bar(BAR_QFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
+        if (qc) mbar_wait(bar(BAR_QFULL), (uint32_t)(qc - 1) & 1u, abort);
         for (int c = kc > 2 ? kc - 2 : 0; c < kc; ++c)
           mbar_wait(bar(BAR_KFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
       }
     }
   } else {
-    // ------------------------------------------------ loads of the blocks' sums
+    // ------------------------------------------------ loads of v and the blocks' sums
     if (lane == 0) {
       const SsmPrep* from =
           ba.prep + (ssm_first_block(a.seq, b) + (row0 - seq0) / SB_L) * a.H + h;
-      int n = 0;
+      int pc = 0, vc = 0;  // blocks whose load is issued
       for (int c = 0; c < nb; ++c) {
         const uint32_t slot = c & 3;
+        const int r = (int)(row0 + (long long)c * SB_L);
         if (c >= 4 && !wait(BAR_PREPFREE + slot, (c >> 2) - 1)) break;
         mbar_expect(bar(BAR_PREP + slot), sizeof(SsmPrep));
         bulk_load(base + SB_PREP + slot * sizeof(SsmPrep), from + (size_t)c * a.H,
                   sizeof(SsmPrep), bar(BAR_PREP + slot));
-        n = c + 1;
+        pc = c + 1;
+        if (c >= 4 && !wait(BAR_VFREE + slot, (c >> 2) - 1)) break;
+        mbar_expect(bar(BAR_VFULL + slot), SB_PANEL);
+        tma_load_3d(base + SB_V + slot * SB_PANEL, &ba.mv, p0, h, r, bar(BAR_VFULL + slot));
+        vc = c + 1;
       }
-      if (*abort)
-        for (int c = n > 4 ? n - 4 : 0; c < n; ++c)
+      if (*abort) {
+        // loads in flight land before the block's memory is given up (each wait limited)
+        for (int c = pc > 4 ? pc - 4 : 0; c < pc; ++c)
           mbar_wait(bar(BAR_PREP + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
+        for (int c = vc > 4 ? vc - 4 : 0; c < vc; ++c)
+          mbar_wait(bar(BAR_VFULL + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
+      }
     }
   }
   }
