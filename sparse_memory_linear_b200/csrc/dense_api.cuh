@@ -213,13 +213,14 @@ bool ssm_block_fits(const sdm_ssm_shape& s, long long R) {
 }
 
 // How a scan cuts sequences into segments.  A CTA walks a segment `unit` rows at a time in about
-// walk_us, `slots` CTAs at once; the pass that makes the segments' own contributions costs pre_us
-// a unit, and with the chain over segments split_us at least.  The number of segments is the one
+// walk_us each and walk_piece_us for all, `slots` CTAs at once; the pass that makes the segments'
+// own contributions costs pre_us a unit and pre_piece_us a segment, and with the chain over
+// segments split_us at least.  The number of segments is the one
 // with the least estimated time; packed batches, whose lengths only the device knows, are cut
 // as one sequence of all rows would be.
 struct SsmCost {
   int unit, slots;
-  double walk_us, pre_us, split_us;
+  double walk_us, walk_piece_us, pre_us, pre_piece_us, split_us;
 };
 
 struct SsmPlan {
@@ -234,13 +235,13 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, c
     return (double)((items * ctas_per_item + c.slots - 1) / c.slots);
   };
   long long best = 1;
-  double least = waves(seqs) * L * c.walk_us;
+  double least = waves(seqs) * (L * c.walk_us + c.walk_piece_us);
   const long long most = 6LL * c.slots / (seqs * ctas_per_item) + 1;  // more waves gain nothing
   for (long long n = 2; n <= L && n <= most; n += n < 16 ? 1 : n / 16) {
     const long long len = (L + n - 1) / n;
     if ((L + len - 1) / len != n) continue;
-    const double t = waves(seqs * n) * len * c.walk_us + waves(seqs * (n - 1)) * len * c.pre_us +
-                     c.split_us;
+    const double t = waves(seqs * n) * (len * c.walk_us + c.walk_piece_us) +
+                     waves(seqs * (n - 1)) * (len * c.pre_us + c.pre_piece_us) + c.split_us;
     if (t < least) {
       least = t;
       best = n;
@@ -261,9 +262,9 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, c
 SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
   if (!block)
     return ssm_plan(s, packed, (long long)s.H * ((s.d_v + SSM_COLS - 1) / SSM_COLS),
-                    SsmCost{16, 5 * sms, 1.6, 1.2, 12.0});
+                    SsmCost{16, 5 * sms, 1.6, 2.0, 1.2, 2.0, 8.0});
   SsmPlan p = ssm_plan(s, packed, (long long)s.H * ((s.d_v + SB_P - 1) / SB_P),
-                       SsmCost{SB_L, sms, 3.3, 1.0, 12.0});
+                       SsmCost{SB_L, sms, 3.1, 1.0, 1.2, 4.0, 8.0});
   // every block's sums, where ssm_first_block puts them
   const long long blocks = packed ? s.T / SB_L + s.B + 1
                                   : s.B * (((long long)s.T + SB_L - 1) / SB_L);
@@ -329,6 +330,7 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
     return SDM_ERR_CUDA;
   const long long blocks = plan.items * s.H * ba.ptiles;
   if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;
+  ba.pieces = (int)blocks;
   const long long preps = plan.items * (plan.seg_rows / SB_L);
   if (preps > 2147483647LL) return SDM_ERR_UNSUPPORTED;
   SDM_CUDA_TRY(launch_pdl<true>(ssm_prep_kernel, dim3((unsigned)preps, (unsigned)(s.H + 7) / 8),
@@ -340,7 +342,8 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
     g_launches.fetch_add(1, std::memory_order_relaxed);
     SDM_CUDA_TRY(launch_ssm_chain(s, a, ba.sp, st));
   }
-  SDM_CUDA_TRY(launch_pdl(ssm_block_kernel, dim3((unsigned)blocks), dim3(SB_THREADS),
+  const unsigned ctas = (unsigned)(blocks < di->sms ? blocks : di->sms);
+  SDM_CUDA_TRY(launch_pdl(ssm_block_kernel, dim3(ctas), dim3(SB_THREADS),
                           (size_t)SB_SMEM, st, ba));
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return SDM_OK;

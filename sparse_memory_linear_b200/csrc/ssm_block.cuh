@@ -14,8 +14,8 @@
 // weight in another's read (half a step of bf16); two parts of M keep the second term below
 // that.
 //
-// One CTA walks the blocks of (sequence segment, head, 64 value columns) in order, five groups of
-// four warps each at its own block:
+// One CTA walks the blocks of its (sequence segment, head, 64 value columns) pieces in order, four
+// groups of four warps each at its own block:
 //   P   a thread per token row: weighs S into P (tensor memory, in place)
 //   Y   a thread per token row: y = exp(c_t) Y2 + Y1 + D v, gated and stored
 //   H   a thread per state row: adds dM to the decayed state, publishes the state's two parts
@@ -84,6 +84,7 @@ struct SsmBlockArgs {
   SsmSplit sp;      // segments of whole blocks
   SsmPrep* prep;    // [blocks, H]
   int ptiles;       // 64-column tiles of d_v
+  int pieces;       // items x H x ptiles
 };
 
 // The place of a sequence's first block among all blocks' sums: sequences of T rows one after
@@ -217,52 +218,42 @@ __device__ __forceinline__ void ssm_store_parts(uint8_t* place, uint32_t o0, uin
   }
 }
 
+// One piece of the scan's work: a segment of a sequence, a head and 64 of its columns.
+struct SsmPiece {
+  long long item, seq0, seq1, row0, row1;
+  int b, h, p0, nb;  // nb blocks
+};
+// Called by a whole warp; false past the last.
+__device__ __forceinline__ bool ssm_piece(const SsmBlockArgs& ba, long long i, SsmPiece& w) {
+  const SsmArgs& a = ba.a;
+  const int per_item = a.H * ba.ptiles;
+  if (i >= ba.pieces) return false;
+  w.item = (unsigned)i / (unsigned)per_item;
+  const int hp = (int)(i - w.item * per_item);
+  w.h = hp / ba.ptiles;
+  w.p0 = (hp - w.h * ba.ptiles) * SB_P;
+  long long seg = 0;
+  if (!ssm_find_item(a.seq, w.item, ba.sp.seg_rows, &w.b, &seg)) return false;
+  w.seq0 = a.seq.start(w.b);
+  w.seq1 = a.seq.end(w.b);
+  w.row0 = w.seq0 + seg * ba.sp.seg_rows;
+  w.row1 = w.row0 + ba.sp.seg_rows < w.seq1 ? w.row0 + ba.sp.seg_rows : w.seq1;
+  w.nb = (int)((w.row1 - w.row0 + SB_L - 1) / SB_L);
+  return true;
+}
+
 __global__ void __launch_bounds__(SB_THREADS, 1)
     ssm_block_kernel(const __grid_constant__ SsmBlockArgs ba) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_abort;
-  __shared__ int s_item_ok, s_b;
-  __shared__ long long s_seg;
   const SsmArgs& a = ba.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const sm = smem_raw + (base - smem_addr(smem_raw));
   const uint32_t bars = base + SB_BARS;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
-
   if (blockIdx.x == 0) a.seq.check();
-  const int per_item = a.H * ba.ptiles;
-  const long long item = blockIdx.x / per_item;
-  const int hp = blockIdx.x % per_item, h = hp / ba.ptiles, p0 = hp % ba.ptiles * SB_P;
-  const int g = h / (a.H / a.G);
-  const long long seg_rows = ba.sp.seg_rows;
-  if (warp == 0) {
-    int b = 0;
-    long long s = 0;
-    const bool ok = ssm_find_item(a.seq, item, seg_rows, &b, &s);
-    if (lane == 0) {
-      s_item_ok = ok;
-      s_b = b;
-      s_seg = s;
-      s_abort = 0;
-    }
-  }
-  __syncthreads();
-  if (!s_item_ok) return;
-  const int b = s_b;
-  const long long seq0 = a.seq.start(b), seq1 = a.seq.end(b);
-  const long long row0 = seq0 + s_seg * seg_rows;
-  const long long row1 = row0 + seg_rows < seq1 ? row0 + seg_rows : seq1;
-  const int nb = (int)((row1 - row0 + SB_L - 1) / SB_L);
-  float* const Mp = a.M + ((size_t)b * a.H + h) * a.N * a.P;
-  if (nb == 0) {  // an empty sequence
-    if (a.from_zero)
-      for (int i = tid; i < a.N * SB_P; i += SB_THREADS) {
-        const int p = p0 + i % SB_P;
-        if (p < a.P) Mp[(size_t)(i / SB_P) * a.P + p] = 0.0f;
-      }
-    return;
-  }
+  if (tid == 0) s_abort = 0;
   const int npanels = a.N > 64 ? 2 : 1, nk = (a.N + 15) / 16;
 
   if (warp == 0) tmem_alloc(base + SB_TMEM_PTR, 512);
@@ -306,19 +297,29 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   tc_fence_after();
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + SB_TMEM_PTR);
   volatile int* const abort = &s_abort;
-  // phase of the c-th use of a barrier that completes once per block, or per two of them
+  // use: how many times the barrier completed before
   auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u, abort); };
   auto prep = [&](int c) {
     return reinterpret_cast<SsmPrep*>(sm + SB_PREP + (c & 3) * sizeof(SsmPrep));
   };
 
+  // The CTA's work: every gridDim.x-th of the (sequence, segment, head, tile) pieces.  Each group
+  // walks them on its own; u0 counts the blocks of the pieces before, for the barriers' phases.
+  // With a CTA per piece a short piece cost more in filling the pipeline than in its blocks.
+  SsmPiece w;
+  bool ok = true;
+  int u0 = 0;
+  auto next_piece = [&](long long i) { return ok && ssm_piece(ba, i, w); };
+
   if (warp < 4) {
     // ------------------------------------------------ P: row t = tid
     const int t = tid;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    for (int c = 0; c < nb; ++c) {
+    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (int c = u0; c < u0 + w.nb; ++c) {
       const uint32_t stage = c & 1;
-      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_S + stage, c >> 1)) break;
+      ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_S + stage, c >> 1);
+      if (!ok) break;
       tc_fence_after();
       const SsmPrep& pr = *prep(c);
       const uint32_t sbuf = tm + TM_S + stage * 128 + lanes;
@@ -401,22 +402,24 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     // ------------------------------------------------ Y: row t = tid - 128
     const int t = tid - 128, quad = warp - 4;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const float D = a.D ? a.D[h] : 0.0f;
+    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    const float D = a.D ? a.D[w.h] : 0.0f;
     const float2 D2 = make_float2(D, D);
-    const int pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;  // columns that exist
-    __nv_bfloat16* const yp = static_cast<__nv_bfloat16*>(a.y) + (size_t)h * a.P + p0;
+    const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;  // columns that exist
+    __nv_bfloat16* const yp = static_cast<__nv_bfloat16*>(a.y) + (size_t)w.h * a.P + w.p0;
     const __nv_bfloat16* const zp =
-        a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)h * a.P + p0 : nullptr;
+        a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)w.h * a.P + w.p0 : nullptr;
     // whole sectors where rows start on them and hold a multiple of 16 values
     const bool sectors = a.P % 16 == 0 && a.gate_stride % 16 == 0 &&
                          ((reinterpret_cast<uintptr_t>(yp) | reinterpret_cast<uintptr_t>(zp)) & 31) == 0;
-    for (int c = 0; c < nb; ++c) {
+    for (int c = u0; c < u0 + w.nb; ++c) {
       const uint32_t stage = c & 1;
-      const long long row = row0 + (long long)c * SB_L + t;
-      const bool live = row < row1;
+      const long long row = w.row0 + (long long)(c - u0) * SB_L + t;
+      const bool live = row < w.row1;
       const __nv_bfloat16* const zrow = zp + row * a.gate_stride;
       __nv_bfloat16* const yrow = yp + (size_t)row * a.H * a.P;
-      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_VFULL + (c & 3), c >> 2)) break;
+      ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
+      if (!ok) break;
       float decay;  // from the block's start up to t
       {
         const SsmPrep& pr = *prep(c);
@@ -440,9 +443,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             *reinterpret_cast<uint4*>(z + 4) = *reinterpret_cast<const uint4*>(zrow + 16 * part + 8);
         }
       };
-      if (zp && row + 2 * SB_L < row1) prefetch_l2(zrow + 2 * SB_L * a.gate_stride);
+      if (zp && row + 2 * SB_L < w.row1) prefetch_l2(zrow + 2 * SB_L * a.gate_stride);
       load_z(0);  // on its way while the products finish
-      if (!wait(BAR_Y2 + stage, c >> 1) || !wait(BAR_Y + stage, c >> 1)) break;
+      ok = wait(BAR_Y2 + stage, c >> 1) && wait(BAR_Y + stage, c >> 1);
+      if (!ok) break;
       tc_fence_after();
       const uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
       const uint32_t ybuf = tm + TM_S + stage * 128 + TM_Y1 + lanes, y2buf = tm + TM_Y2 + stage * 64 + lanes;
@@ -491,24 +495,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         mbar_arrive(bar(BAR_VFREE + (c & 3)));
       }
     }
+    }
   } else if (warp < 12) {
     // ------------------------------------------------ H: row n = tid - 256
     const int n = tid - 256;
     const uint32_t lanes = (uint32_t)((warp - 8) * 32) << 16;
-    const int pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;
-    float* const mrow = Mp + (size_t)n * a.P + p0;
-    const bool split = seq1 - seq0 > seg_rows;
-    const float* const from =
-        split ? ba.sp.starts + (((size_t)item * a.H + h) * a.N + n) * a.P + p0 : mrow;
     float2 st[SB_P / 2];
-#pragma unroll
-    for (int i = 0; i < SB_P; i += 4) {
-      float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-      if ((split || !a.from_zero) && n < a.N && i < pn)
-        m = *reinterpret_cast<const float4*>(from + i);
-      st[i / 2] = make_float2(m.x, m.y);
-      st[i / 2 + 1] = make_float2(m.z, m.w);
-    }
     // two bf16 parts of eight of the row's values, as a chunk of the B operand of Y2
     auto publish = [&](int ch) {
       uint32_t u[4], v[4];
@@ -529,11 +521,28 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_HREADY));
     };
+    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
+    float* const mrow = a.M + (((size_t)w.b * a.H + w.h) * a.N + n) * a.P + w.p0;
+    const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
+    const float* const from =
+        split ? ba.sp.starts + (((size_t)w.item * a.H + w.h) * a.N + n) * a.P + w.p0 : mrow;
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch) publish(ch);
-    published();
-    bool ok = true;
-    for (int c = 0; c < nb; ++c) {
+    for (int i = 0; i < SB_P; i += 4) {
+      float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+      if ((split || !a.from_zero) && n < a.N && i < pn)
+        m = *reinterpret_cast<const float4*>(from + i);
+      st[i / 2] = make_float2(m.x, m.y);
+      st[i / 2 + 1] = make_float2(m.z, m.w);
+    }
+    if (w.nb > 0) {  // the state before the piece; the last block before has read its own
+      ok = u0 == 0 || wait(BAR_HFREE, u0 - 1);
+      if (!ok) break;
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) publish(ch);
+      published();
+    }
+    for (int c = u0; c < u0 + w.nb; ++c) {
       ok = wait(BAR_PREP + (c & 3), c >> 2);
       if (!ok) break;
       const SsmPrep& pr = *prep(c);
@@ -558,7 +567,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_DMFREE + (c & 1)));
-      if (c + 1 < nb) {
+      if (c + 1 < u0 + w.nb) {
         ok = wait(BAR_HFREE, c);
         if (!ok) break;
 #pragma unroll
@@ -566,26 +575,30 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         published();
       }
     }
-    if (ok && row1 == seq1 && n < a.N) {
+    if (ok && w.row1 == w.seq1 && n < a.N) {
 #pragma unroll
       for (int i = 0; i < SB_P; i += 4)
         if (i < pn)
           *reinterpret_cast<float4*>(mrow + i) =
               make_float4(st[i / 2].x, st[i / 2].y, st[i / 2 + 1].x, st[i / 2 + 1].y);
     }
+    }
   } else if (warp < 16) {
     // ------------------------------------------------ W: three bf16 parts of w o v
     const int i0 = tid - 384, rq = i0 >> 2;  // row in the quarter, and 16 of its values
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
-    for (int c = 0; c < nb; ++c) {
+    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (int c = u0; c < u0 + w.nb; ++c) {
       const int stage = c & 1;
-      if (!wait(BAR_PREP + (c & 3), c >> 2) || !wait(BAR_VFULL + (c & 3), c >> 2)) break;
+      ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
+      if (!ok) break;
       uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
-      const float* w = prep(c)->w;
-      const long long left = row1 - (row0 + (long long)c * SB_L);
+      const float* weights = prep(c)->w;
+      const long long left = w.row1 - (w.row0 + (long long)(c - u0) * SB_L);
       if (left < SB_L) {
         // rows behind the segment's end, whatever they hold, become zeros
-        if (!wait(BAR_KFULL + stage, c >> 1)) break;
+        ok = wait(BAR_KFULL + stage, c >> 1);
+        if (!ok) break;
         for (int t = rq; t < SB_L; t += 32) {
           if (t < left) continue;
           for (int i = 0; i < 2; ++i) {
@@ -597,10 +610,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           }
         }
       }
-      bool ok = true;
       uint4 na = *reinterpret_cast<const uint4*>(vtile + o0),
             nb4 = *reinterpret_cast<const uint4*>(vtile + o1);
-      float nw = w[rq];
+      float nw = weights[rq];
 #pragma unroll 1
       for (int qd = 0; qd < 4; ++qd) {
         const int use = 4 * c + qd, buf = qd & 1;
@@ -609,7 +621,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (qd < 3) {
           na = *reinterpret_cast<const uint4*>(vtile + 4096 * (qd + 1) + o0);
           nb4 = *reinterpret_cast<const uint4*>(vtile + 4096 * (qd + 1) + o1);
-          nw = w[32 * (qd + 1) + rq];
+          nw = weights[32 * (qd + 1) + rq];
         }
         ok = use < 2 || wait(BAR_WFREE + buf, (use >> 1) - 1);
         if (!ok) break;
@@ -627,11 +639,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY2 = mma_desc(128, 64, 0, 1);
     const uint32_t q0 = tile_desc(base + SB_Q), k0 = tile_desc(base + SB_K),
                    h0 = tile_desc(base + SB_H);
-    for (int c = -1; c < nb; ++c) {
-      if (c >= 0) {
+    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (int c = u0 - 1; c < u0 + w.nb; ++c) {
+      if (c >= u0) {
         const uint32_t stage = c & 1;
         // the block's buffer of Y2 is free since its S was issued: group Y reads both
-        if (!wait(BAR_HREADY, c)) break;
+        ok = wait(BAR_HREADY, c);
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -648,11 +662,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         __syncwarp();
       }
       const int e = c + 1;
-      if (e < nb) {
+      if (e < u0 + w.nb) {
         const uint32_t stage = e & 1;
-        if (!wait(BAR_QFULL, e) || !wait(BAR_KFULL + stage, e >> 1) ||
-            (e >= 2 && !wait(BAR_YFREE + stage, (e >> 1) - 1)))
-          break;
+        ok = wait(BAR_QFULL, e) && wait(BAR_KFULL + stage, e >> 1) &&
+             (e < 2 || wait(BAR_YFREE + stage, (e >> 1) - 1));
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t k = k0 + stage * (2 * SB_PANEL >> 4);
@@ -675,8 +689,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     constexpr uint32_t dM = mma_desc(128, 64, 1, 1), dY1 = mma_desc(128, 64, 0, 1);
     const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W),
                    v0 = tile_desc(base + SB_V);
-    bool ok = true;
-    for (int c = 0; c < nb && ok; ++c) {
+    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (int c = u0; c < u0 + w.nb && ok; ++c) {
       const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
       ok = wait(BAR_KFULL + stage, c >> 1) &&
            (c < 2 || wait(BAR_DMFREE + stage, (c >> 1) - 1));
@@ -686,11 +700,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t kq = k + qd * (4096 >> 4), w = w0 + buf * (3 * SB_WPART >> 4);
+          const uint32_t kq = k + qd * (4096 >> 4), wb = w0 + buf * (3 * SB_WPART >> 4);
 #pragma unroll
           for (int i = 0; i < 6; ++i)
             mma_ss(tm + TM_DM + stage * 64, kq + (i & 1) * (2048 >> 4),
-                   w + (((i >> 1) * SB_WPART + (i & 1) * 2048) >> 4), dM, qd + i > 0);
+                   wb + (((i >> 1) * SB_WPART + (i & 1) * 2048) >> 4), dM, qd + i > 0);
           mma_commit(bar(BAR_WFREE + buf));
           if (qd == 3) {
             mma_commit(bar(BAR_DM + stage));
@@ -717,56 +731,66 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     mbar_wait(bar(BAR_DRAIN + 1), 0, abort);
   } else if (warp == 19) {
     // ------------------------------------------------ loads of k and q
-    if (lane == 0) {
-      int kc = 0, qc = 0;  // blocks whose load is issued
-      for (int c = 0; c < nb; ++c) {
-        const uint32_t stage = c & 1;
-        const int r = (int)(row0 + (long long)c * SB_L);
-        if (c >= 2 && !wait(BAR_KFREE + stage, (c >> 1) - 1)) break;
-        mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
-        for (int pl = 0; pl < npanels; ++pl)
-          tma_load_3d(base + SB_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
-                      bar(BAR_KFULL + stage));
-        kc = c + 1;
-        if (c >= 1 && !wait(BAR_QFREE, c - 1)) break;
-        mbar_expect(bar(BAR_QFULL), npanels * SB_PANEL);
-        for (int pl = 0; pl < npanels; ++pl)
-          tma_load_3d(base + SB_Q + pl * SB_PANEL, &ba.mq, 64 * pl, g, r, bar(BAR_QFULL));
-        qc = c + 1;
+    int kc = 0, qc = 0;  // blocks whose load is issued
+    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+      if (lane == 0) {
+        const int g = w.h / (a.H / a.G);
+        for (int c = u0; c < u0 + w.nb; ++c) {
+          const uint32_t stage = c & 1;
+          const int r = (int)(w.row0 + (long long)(c - u0) * SB_L);
+          ok = c < 2 || wait(BAR_KFREE + stage, (c >> 1) - 1);
+          if (!ok) break;
+          mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
+          for (int pl = 0; pl < npanels; ++pl)
+            tma_load_3d(base + SB_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
+                        bar(BAR_KFULL + stage));
+          kc = c + 1;
+          ok = c < 1 || wait(BAR_QFREE, c - 1);
+          if (!ok) break;
+          mbar_expect(bar(BAR_QFULL), npanels * SB_PANEL);
+          for (int pl = 0; pl < npanels; ++pl)
+            tma_load_3d(base + SB_Q + pl * SB_PANEL, &ba.mq, 64 * pl, g, r, bar(BAR_QFULL));
+          qc = c + 1;
+        }
       }
-      if (*abort) {
-        // loads in flight land before the block's memory is given up (each wait limited)
-        if (qc) mbar_wait(bar(BAR_QFULL), (uint32_t)(qc - 1) & 1u, abort);
-        for (int c = kc > 2 ? kc - 2 : 0; c < kc; ++c)
-          mbar_wait(bar(BAR_KFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
-      }
+      ok = __shfl_sync(FULL_MASK, (int)ok, 0);
+    }
+    if (*abort && lane == 0) {
+      // loads in flight land before the block's memory is given up (each wait limited)
+      if (qc) mbar_wait(bar(BAR_QFULL), (uint32_t)(qc - 1) & 1u, abort);
+      for (int c = kc > 2 ? kc - 2 : 0; c < kc; ++c)
+        mbar_wait(bar(BAR_KFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
     }
   } else {
     // ------------------------------------------------ loads of v and the blocks' sums
-    if (lane == 0) {
-      const SsmPrep* from =
-          ba.prep + (ssm_first_block(a.seq, b) + (row0 - seq0) / SB_L) * a.H + h;
-      int pc = 0, vc = 0;  // blocks whose load is issued
-      for (int c = 0; c < nb; ++c) {
-        const uint32_t slot = c & 3;
-        const int r = (int)(row0 + (long long)c * SB_L);
-        if (c >= 4 && !wait(BAR_PREPFREE + slot, (c >> 2) - 1)) break;
-        mbar_expect(bar(BAR_PREP + slot), sizeof(SsmPrep));
-        bulk_load(base + SB_PREP + slot * sizeof(SsmPrep), from + (size_t)c * a.H,
-                  sizeof(SsmPrep), bar(BAR_PREP + slot));
-        pc = c + 1;
-        if (c >= 4 && !wait(BAR_VFREE + slot, (c >> 2) - 1)) break;
-        mbar_expect(bar(BAR_VFULL + slot), SB_PANEL);
-        tma_load_3d(base + SB_V + slot * SB_PANEL, &ba.mv, p0, h, r, bar(BAR_VFULL + slot));
-        vc = c + 1;
+    int pc = 0, vc = 0;  // blocks whose load is issued
+    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+      if (lane == 0) {
+        const SsmPrep* from =
+            ba.prep + (ssm_first_block(a.seq, w.b) + (w.row0 - w.seq0) / SB_L) * a.H + w.h;
+        for (int c = u0; c < u0 + w.nb; ++c) {
+          const uint32_t slot = c & 3;
+          const int r = (int)(w.row0 + (long long)(c - u0) * SB_L);
+          ok = c < 4 || wait(BAR_PREPFREE + slot, (c >> 2) - 1);
+          if (!ok) break;
+          mbar_expect(bar(BAR_PREP + slot), sizeof(SsmPrep));
+          bulk_load(base + SB_PREP + slot * sizeof(SsmPrep), from + (size_t)(c - u0) * a.H,
+                    sizeof(SsmPrep), bar(BAR_PREP + slot));
+          pc = c + 1;
+          ok = c < 4 || wait(BAR_VFREE + slot, (c >> 2) - 1);
+          if (!ok) break;
+          mbar_expect(bar(BAR_VFULL + slot), SB_PANEL);
+          tma_load_3d(base + SB_V + slot * SB_PANEL, &ba.mv, w.p0, w.h, r, bar(BAR_VFULL + slot));
+          vc = c + 1;
+        }
       }
-      if (*abort) {
-        // loads in flight land before the block's memory is given up (each wait limited)
-        for (int c = pc > 4 ? pc - 4 : 0; c < pc; ++c)
-          mbar_wait(bar(BAR_PREP + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
-        for (int c = vc > 4 ? vc - 4 : 0; c < vc; ++c)
-          mbar_wait(bar(BAR_VFULL + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
-      }
+      ok = __shfl_sync(FULL_MASK, (int)ok, 0);
+    }
+    if (*abort && lane == 0) {
+      for (int c = pc > 4 ? pc - 4 : 0; c < pc; ++c)
+        mbar_wait(bar(BAR_PREP + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
+      for (int c = vc > 4 ? vc - 4 : 0; c < vc; ++c)
+        mbar_wait(bar(BAR_VFULL + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
     }
   }
   }
