@@ -226,7 +226,7 @@ struct SsmCost {
 struct SsmPlan {
   long long seg_rows, items;  // rows of a segment; (sequence, segment) pairs at most
   bool split;
-  size_t off_decays, off_prep, bytes;
+  size_t off_decays, off_prep, off_items, bytes;
 };
 
 SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, const SsmCost& c) {
@@ -269,7 +269,8 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
   const long long blocks = packed ? s.T / SB_L + s.B + 1
                                   : s.B * (((long long)s.T + SB_L - 1) / SB_L);
   p.off_prep = p.bytes;
-  p.bytes += round_up((size_t)blocks * s.H * sizeof(SsmPrep), WS_ALIGN);
+  p.off_items = p.bytes + round_up((size_t)blocks * s.H * sizeof(SsmPrep), WS_ALIGN);
+  p.bytes = p.off_items + round_up((size_t)p.items * sizeof(int4), WS_ALIGN);
   return p;
 }
 
@@ -323,10 +324,12 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
   ba.a = a;
   ba.sp = ssm_split(plan, ws);
   ba.prep = reinterpret_cast<SsmPrep*>(static_cast<char*>(ws) + plan.off_prep);
+  ba.items = reinterpret_cast<int4*>(static_cast<char*>(ws) + plan.off_items);
   ba.ptiles = (s.d_v + SB_P - 1) / SB_P;
   if (!tile_map(&ba.mq, a.q, s.N, s.G, a.seq.R, a.q_stride) ||
       !tile_map(&ba.mk, a.k, s.N, s.G, a.seq.R, a.k_stride) ||
-      !tile_map(&ba.mv, a.v, s.d_v, s.H, a.seq.R, a.v_stride))
+      !tile_map(&ba.mv, a.v, s.d_v, s.H, a.seq.R, a.v_stride) ||
+      (a.gate && !tile_map(&ba.mz, a.gate, s.d_v, s.H, a.seq.R, a.gate_stride)))
     return SDM_ERR_CUDA;
   const long long blocks = plan.items * s.H * ba.ptiles;
   if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;
@@ -334,7 +337,7 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
   const long long preps = plan.items * (plan.seg_rows / SB_L);
   if (preps > 2147483647LL) return SDM_ERR_UNSUPPORTED;
   SDM_CUDA_TRY(launch_pdl<true>(ssm_prep_kernel, dim3((unsigned)preps, (unsigned)(s.H + 7) / 8),
-                                dim3(256), 0, st, a, ba.sp, ba.prep));
+                                dim3(256), 0, st, a, ba.sp, ba.prep, ba.items));
   g_launches.fetch_add(1, std::memory_order_relaxed);
   if (plan.split) {
     SDM_CUDA_TRY(launch_pdl(ssm_segment_kernel, dim3((unsigned)blocks), dim3(SG_THREADS),

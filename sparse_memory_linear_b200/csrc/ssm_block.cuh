@@ -80,9 +80,10 @@ constexpr float SB_LOG2E = 1.4426950408889634f;
 
 struct SsmBlockArgs {
   SsmArgs a;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mz;  // mz: the gate, where there is one
   SsmSplit sp;      // segments of whole blocks
   SsmPrep* prep;    // [blocks, H]
+  int4* items;      // [items] (sequence, its first and past-last row, the segment's first row)
   int ptiles;       // 64-column tiles of d_v
   int pieces;       // items x H x ptiles
 };
@@ -138,10 +139,12 @@ __device__ __forceinline__ void ssm_sums(const float raw[4], const bool live[4],
   o.tail[3] = after;
 }
 
-// Step sizes and decay sums of every block and head, once for all tiles and passes: a warp per
+// Step sizes and decay sums of every block and head, once for all tiles and passes, and the table
+// of work items (a packed batch's lengths are known only here): a warp per
 // (block, head), a CTA's eight warps on neighbouring heads, whose dt share sectors.  Made inside
 // the scan by one warp a block this was a chain of 3000 cycles, most of a block's time.
-__global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, SsmPrep* prep) {
+__global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, SsmPrep* prep,
+                                                        int4* items) {
   grid_dependency_wait();
   grid_launch_dependents();
   __shared__ int s_ok, s_b;
@@ -161,9 +164,11 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, S
     }
   }
   __syncthreads();
-  if (!s_ok || h >= a.H) return;
-  const long long seq0 = a.seq.start(s_b), seq1 = a.seq.end(s_b);
+  const long long seq0 = s_ok ? a.seq.start(s_b) : 0, seq1 = s_ok ? a.seq.end(s_b) : 0;
   const long long row0 = seq0 + s_seg * sp.seg_rows + (long long)c * SB_L;
+  if (c == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+    items[item] = make_int4(s_ok ? s_b : -1, (int)seq0, (int)seq1, (int)row0);
+  if (!s_ok || h >= a.H) return;
   if (row0 >= seq1) return;
   const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
   const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
@@ -220,25 +225,25 @@ __device__ __forceinline__ void ssm_store_parts(uint8_t* place, uint32_t o0, uin
 
 // One piece of the scan's work: a segment of a sequence, a head and 64 of its columns.
 struct SsmPiece {
-  long long item, seq0, seq1, row0, row1;
-  int b, h, p0, nb;  // nb blocks
+  int item, b, seq0, seq1, row0, row1, h, p0, nb;  // nb blocks
 };
-// Called by a whole warp; false past the last.
-__device__ __forceinline__ bool ssm_piece(const SsmBlockArgs& ba, long long i, SsmPiece& w) {
-  const SsmArgs& a = ba.a;
-  const int per_item = a.H * ba.ptiles;
+// False past the last.
+__device__ __forceinline__ bool ssm_piece(const SsmBlockArgs& ba, int i, SsmPiece& w) {
   if (i >= ba.pieces) return false;
-  w.item = (unsigned)i / (unsigned)per_item;
-  const int hp = (int)(i - w.item * per_item);
+  const int per_item = ba.a.H * ba.ptiles;
+  w.item = i / per_item;
+  const int hp = i - w.item * per_item;
   w.h = hp / ba.ptiles;
   w.p0 = (hp - w.h * ba.ptiles) * SB_P;
-  long long seg = 0;
-  if (!ssm_find_item(a.seq, w.item, ba.sp.seg_rows, &w.b, &seg)) return false;
-  w.seq0 = a.seq.start(w.b);
-  w.seq1 = a.seq.end(w.b);
-  w.row0 = w.seq0 + seg * ba.sp.seg_rows;
-  w.row1 = w.row0 + ba.sp.seg_rows < w.seq1 ? w.row0 + ba.sp.seg_rows : w.seq1;
-  w.nb = (int)((w.row1 - w.row0 + SB_L - 1) / SB_L);
+  const int4 at = __ldg(ba.items + w.item);
+  if (at.x < 0) return false;
+  w.b = at.x;
+  w.seq0 = at.y;
+  w.seq1 = at.z;
+  w.row0 = at.w;
+  const int left = w.seq1 - w.row0;
+  w.row1 = w.row0 + (left < ba.sp.seg_rows ? left : (int)ba.sp.seg_rows);
+  w.nb = (w.row1 - w.row0 + SB_L - 1) / SB_L;
   return true;
 }
 
@@ -309,13 +314,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   SsmPiece w;
   bool ok = true;
   int u0 = 0;
-  auto next_piece = [&](long long i) { return ok && ssm_piece(ba, i, w); };
+  auto next_piece = [&](int i) { return ok && ssm_piece(ba, i, w); };
 
   if (warp < 4) {
     // ------------------------------------------------ P: row t = tid
     const int t = tid;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
     for (int c = u0; c < u0 + w.nb; ++c) {
       const uint32_t stage = c & 1;
       ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_S + stage, c >> 1);
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     // ------------------------------------------------ Y: row t = tid - 128
     const int t = tid - 128, quad = warp - 4;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
     const float D = a.D ? a.D[w.h] : 0.0f;
     const float2 D2 = make_float2(D, D);
     const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;  // columns that exist
@@ -414,9 +419,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                          ((reinterpret_cast<uintptr_t>(yp) | reinterpret_cast<uintptr_t>(zp)) & 31) == 0;
     for (int c = u0; c < u0 + w.nb; ++c) {
       const uint32_t stage = c & 1;
-      const long long row = w.row0 + (long long)(c - u0) * SB_L + t;
+      const int row = w.row0 + (c - u0) * SB_L + t;
       const bool live = row < w.row1;
-      const __nv_bfloat16* const zrow = zp + row * a.gate_stride;
+      const __nv_bfloat16* const zrow = zp + (long long)row * a.gate_stride;
       __nv_bfloat16* const yrow = yp + (size_t)row * a.H * a.P;
       ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
       if (!ok) break;
@@ -443,7 +448,6 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             *reinterpret_cast<uint4*>(z + 4) = *reinterpret_cast<const uint4*>(zrow + 16 * part + 8);
         }
       };
-      if (zp && row + 2 * SB_L < w.row1) prefetch_l2(zrow + 2 * SB_L * a.gate_stride);
       load_z(0);  // on its way while the products finish
       ok = wait(BAR_Y2 + stage, c >> 1) && wait(BAR_Y + stage, c >> 1);
       if (!ok) break;
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_HREADY));
     };
-    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
     const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
     float* const mrow = a.M + (((size_t)w.b * a.H + w.h) * a.N + n) * a.P + w.p0;
     const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
@@ -587,14 +591,14 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     // ------------------------------------------------ W: three bf16 parts of w o v
     const int i0 = tid - 384, rq = i0 >> 2;  // row in the quarter, and 16 of its values
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
-    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
     for (int c = u0; c < u0 + w.nb; ++c) {
       const int stage = c & 1;
       ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
       if (!ok) break;
       uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
       const float* weights = prep(c)->w;
-      const long long left = w.row1 - (w.row0 + (long long)(c - u0) * SB_L);
+      const int left = w.row1 - (w.row0 + (c - u0) * SB_L);
       if (left < SB_L) {
         // rows behind the segment's end, whatever they hold, become zeros
         ok = wait(BAR_KFULL + stage, c >> 1);
@@ -639,7 +643,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY2 = mma_desc(128, 64, 0, 1);
     const uint32_t q0 = tile_desc(base + SB_Q), k0 = tile_desc(base + SB_K),
                    h0 = tile_desc(base + SB_H);
-    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
     for (int c = u0 - 1; c < u0 + w.nb; ++c) {
       if (c >= u0) {
         const uint32_t stage = c & 1;
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     constexpr uint32_t dM = mma_desc(128, 64, 1, 1), dY1 = mma_desc(128, 64, 0, 1);
     const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W),
                    v0 = tile_desc(base + SB_V);
-    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
     for (int c = u0; c < u0 + w.nb && ok; ++c) {
       const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
       ok = wait(BAR_KFULL + stage, c >> 1) &&
@@ -732,12 +736,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   } else if (warp == 19) {
     // ------------------------------------------------ loads of k and q
     int kc = 0, qc = 0;  // blocks whose load is issued
-    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
       if (lane == 0) {
         const int g = w.h / (a.H / a.G);
         for (int c = u0; c < u0 + w.nb; ++c) {
           const uint32_t stage = c & 1;
-          const int r = (int)(w.row0 + (long long)(c - u0) * SB_L);
+          const int r = w.row0 + (c - u0) * SB_L;
           ok = c < 2 || wait(BAR_KFREE + stage, (c >> 1) - 1);
           if (!ok) break;
           mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
@@ -764,13 +768,24 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   } else {
     // ------------------------------------------------ loads of v and the blocks' sums
     int pc = 0, vc = 0;  // blocks whose load is issued
-    for (long long piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+      // what groups H and Y read on their own comes into the L2 ahead of them: the state before
+      // the piece, and block by block the gate
+      const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
+      if (w.nb > 0 && (split || !a.from_zero)) {
+        const float* m = (split ? ba.sp.starts + ((size_t)w.item * a.H + w.h) * a.N * a.P
+                                : a.M + ((size_t)w.b * a.H + w.h) * a.N * a.P) + w.p0;
+        const int bytes = 4 * (a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P);
+        for (int n = lane; n < a.N; n += 32)
+          for (int o = 0; o < bytes; o += 128)
+            prefetch_l2(reinterpret_cast<const char*>(m + (size_t)n * a.P) + o);
+      }
       if (lane == 0) {
         const SsmPrep* from =
             ba.prep + (ssm_first_block(a.seq, w.b) + (w.row0 - w.seq0) / SB_L) * a.H + w.h;
         for (int c = u0; c < u0 + w.nb; ++c) {
           const uint32_t slot = c & 3;
-          const int r = (int)(w.row0 + (long long)(c - u0) * SB_L);
+          const int r = w.row0 + (c - u0) * SB_L;
           ok = c < 4 || wait(BAR_PREPFREE + slot, (c >> 2) - 1);
           if (!ok) break;
           mbar_expect(bar(BAR_PREP + slot), sizeof(SsmPrep));
@@ -781,6 +796,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           if (!ok) break;
           mbar_expect(bar(BAR_VFULL + slot), SB_PANEL);
           tma_load_3d(base + SB_V + slot * SB_PANEL, &ba.mv, w.p0, w.h, r, bar(BAR_VFULL + slot));
+          if (a.gate) tma_prefetch_3d(&ba.mz, w.p0, w.h, r);
           vc = c + 1;
         }
       }
