@@ -259,6 +259,11 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, c
   return p;
 }
 
+// Places for blocks' sums (ssm_first_block).
+long long ssm_prep_blocks(const sdm_ssm_shape& s, bool packed) {
+  return packed ? (long long)s.T / SB_L + s.B + 1 : s.B * (((long long)s.T + SB_L - 1) / SB_L);
+}
+
 SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
   if (!block)
     return ssm_plan(s, packed, (long long)s.H * ((s.d_v + SSM_COLS - 1) / SSM_COLS),
@@ -266,8 +271,7 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
   SsmPlan p = ssm_plan(s, packed, (long long)s.H * ((s.d_v + SB_P - 1) / SB_P),
                        SsmCost{SB_L, sms, 3.1, 1.0, 1.2, 4.0, 8.0});
   // every block's sums, where ssm_first_block puts them
-  const long long blocks = packed ? s.T / SB_L + s.B + 1
-                                  : s.B * (((long long)s.T + SB_L - 1) / SB_L);
+  const long long blocks = ssm_prep_blocks(s, packed);
   p.off_prep = p.bytes;
   p.off_items = p.bytes + round_up((size_t)blocks * s.H * sizeof(SsmPrep), WS_ALIGN);
   p.bytes = p.off_items + round_up((size_t)p.items * sizeof(int4), WS_ALIGN);
@@ -280,12 +284,12 @@ SsmSplit ssm_split(const SsmPlan& plan, void* ws) {
 }
 
 cudaError_t launch_ssm_chain(const sdm_ssm_shape& s, const SsmArgs& a, const SsmSplit& sp,
-                             cudaStream_t st) {
+                             const DeviceInfo* di, cudaStream_t st) {
+  const long long units = (long long)s.H * ((s.N * s.d_v / 4 + 255) / 256);
+  const long long seqs = a.seq.cu ? 1 : s.B;  // uniform batches: every sequence is split
+  const long long most = 8LL * di->sms, blocks = units * seqs < most ? units : most;
   g_launches.fetch_add(1, std::memory_order_relaxed);
-  return launch_pdl<true>(ssm_chain_kernel,
-                          dim3((unsigned)s.B, (unsigned)s.H,
-                               (unsigned)((s.N * s.d_v / 4 + 255) / 256)),
-                          dim3(256), 0, st, a, sp);
+  return launch_pdl<true>(ssm_chain_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, sp);
 }
 
 template <typename T, bool CONTRIB>
@@ -311,7 +315,7 @@ sdm_status ssm_scan_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceIn
                   (unsigned)((s.d_v + SSM_COLS - 1) / SSM_COLS));
   if (plan.split) {
     SDM_CUDA_TRY((launch_ssm_scan<T, true>(a, sp, grid, st)));
-    SDM_CUDA_TRY(launch_ssm_chain(s, a, sp, st));
+    SDM_CUDA_TRY(launch_ssm_chain(s, a, sp, di, st));
   }
   SDM_CUDA_TRY((launch_ssm_scan<T, false>(a, sp, grid, st)));
   return SDM_OK;
@@ -334,18 +338,20 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
   const long long blocks = plan.items * s.H * ba.ptiles;
   if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;
   ba.pieces = (int)blocks;
-  const long long preps = plan.items * (plan.seg_rows / SB_L);
-  if (preps > 2147483647LL) return SDM_ERR_UNSUPPORTED;
-  SDM_CUDA_TRY(launch_pdl<true>(ssm_prep_kernel, dim3((unsigned)preps, (unsigned)(s.H + 7) / 8),
-                                dim3(256), 0, st, a, ba.sp, ba.prep, ba.items));
+  const unsigned ctas = (unsigned)(blocks < di->sms ? blocks : di->sms);
+  const long long preps = ssm_prep_blocks(s, a.seq.cu != nullptr);
+  SDM_CUDA_TRY(launch_pdl<true>(ssm_prep_kernel,
+                                dim3((unsigned)(preps + (plan.items + 7) / 8),
+                                     (unsigned)(s.H + 7) / 8),
+                                dim3(256), 0, st, a, ba.sp, ba.prep, (int)preps, ba.items,
+                                (int)plan.items));
   g_launches.fetch_add(1, std::memory_order_relaxed);
   if (plan.split) {
-    SDM_CUDA_TRY(launch_pdl(ssm_segment_kernel, dim3((unsigned)blocks), dim3(SG_THREADS),
+    SDM_CUDA_TRY(launch_pdl(ssm_segment_kernel, dim3(ctas), dim3(SG_THREADS),
                             (size_t)SG_SMEM, st, ba));
     g_launches.fetch_add(1, std::memory_order_relaxed);
-    SDM_CUDA_TRY(launch_ssm_chain(s, a, ba.sp, st));
+    SDM_CUDA_TRY(launch_ssm_chain(s, a, ba.sp, di, st));
   }
-  const unsigned ctas = (unsigned)(blocks < di->sms ? blocks : di->sms);
   SDM_CUDA_TRY(launch_pdl(ssm_block_kernel, dim3(ctas), dim3(SB_THREADS),
                           (size_t)SB_SMEM, st, ba));
   g_launches.fetch_add(1, std::memory_order_relaxed);

@@ -283,54 +283,72 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
 }
 
 // The states before the segments of a split sequence, from the first on: what the sequence
-// starts with, then each segment's decay and contribution.  A block per (sequence, head, 1024
-// state values); eight segments' values are on their way at a time.
+// starts with, then each segment's decay and contribution.  Blocks share the (head, 1024 state
+// values) parts of every split sequence; the sequences are looked through 256 at a time, so
+// that a batch of short ones costs next to nothing.  Eight segments' values are on their way at
+// a time.
 __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) {
   grid_dependency_wait();
   grid_launch_dependents();
   __shared__ unsigned long long s_first;
-  const int b = blockIdx.x, h = blockIdx.y, i = blockIdx.z * 256 + threadIdx.x;
-  const long long seg = sp.seg_rows, len = a.seq.end(b) - a.seq.start(b);
-  if (len <= seg) return;
-  if (threadIdx.x == 0) s_first = a.seq.cu ? 0 : b * ((a.seq.T + seg - 1) / seg);
-  __syncthreads();
-  if (a.seq.cu) {
-    long long items = 0;
-    for (int e = threadIdx.x; e < b; e += 256) {
-      const long long n = a.seq.end(e) - a.seq.start(e);
-      items += n > 0 ? (n + seg - 1) / seg : 1;
-    }
-    if (items) atomicAdd(&s_first, (unsigned long long)items);
-  }
-  __syncthreads();
-  const int n4 = a.N * a.P / 4;
-  if (i >= n4) return;
-  const long long first = (long long)s_first;
-  const int segs = (int)((len + seg - 1) / seg);
+  __shared__ int s_split[256];
+  const long long seg = sp.seg_rows;
+  const int n4 = a.N * a.P / 4, parts = (n4 + 255) / 256;
   const size_t step = (size_t)a.H * n4;
-  float4* at = reinterpret_cast<float4*>(sp.starts) + ((size_t)first * a.H + h) * n4 + i;
-  const float* decay = sp.decays + first * a.H + h;
-  float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (!a.from_zero) m = reinterpret_cast<const float4*>(a.M)[((size_t)b * a.H + h) * n4 + i];
-  at[0] = m;
-  for (int s0 = 1; s0 < segs; s0 += 8) {
-    float4 e[8];
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (s0 + j < segs) {
-        e[j] = at[(s0 + j) * step];
-        f[j] = decay[(size_t)(s0 + j - 1) * a.H];
+  auto items_of = [&](int b) {
+    const long long len = a.seq.end(b) - a.seq.start(b);
+    return len > 0 ? (len + seg - 1) / seg : 1;
+  };
+  for (int b0 = 0; b0 < a.seq.B; b0 += 256) {
+    const int e = b0 + (int)threadIdx.x;
+    const int mine = e < a.seq.B && a.seq.end(e) - a.seq.start(e) > seg;
+    s_split[threadIdx.x] = mine;
+    if (!__syncthreads_or(mine)) continue;
+    for (int j = 0; j < 256 && b0 + j < a.seq.B; ++j) {
+      if (!s_split[j]) continue;
+      const int b = b0 + j;
+      __syncthreads();
+      if (threadIdx.x == 0) s_first = a.seq.cu ? 0 : b * items_of(b);
+      __syncthreads();
+      if (a.seq.cu) {
+        unsigned long long items = 0;
+        for (int i = threadIdx.x; i < b; i += 256) items += items_of(i);
+        if (items) atomicAdd(&s_first, items);
       }
+      __syncthreads();
+      const long long first = (long long)s_first;
+      const int segs = (int)items_of(b);
+      for (int unit = blockIdx.x; unit < a.H * parts; unit += gridDim.x) {
+        const int h = unit / parts, i = (unit - h * parts) * 256 + (int)threadIdx.x;
+        if (i >= n4) continue;
+        float4* at = reinterpret_cast<float4*>(sp.starts) + ((size_t)first * a.H + h) * n4 + i;
+        const float* decay = sp.decays + first * a.H + h;
+        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!a.from_zero)
+          m = reinterpret_cast<const float4*>(a.M)[((size_t)b * a.H + h) * n4 + i];
+        at[0] = m;
+        for (int s0 = 1; s0 < segs; s0 += 8) {
+          float4 v[8];
+          float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (s0 + j < segs) {
-        m.x = fmaf(m.x, f[j], e[j].x);
-        m.y = fmaf(m.y, f[j], e[j].y);
-        m.z = fmaf(m.z, f[j], e[j].z);
-        m.w = fmaf(m.w, f[j], e[j].w);
-        at[(s0 + j) * step] = m;
+          for (int x = 0; x < 8; ++x)
+            if (s0 + x < segs) {
+              v[x] = at[(s0 + x) * step];
+              f[x] = decay[(size_t)(s0 + x - 1) * a.H];
+            }
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (s0 + x < segs) {
+              m.x = fmaf(m.x, f[x], v[x].x);
+              m.y = fmaf(m.y, f[x], v[x].y);
+              m.z = fmaf(m.z, f[x], v[x].z);
+              m.w = fmaf(m.w, f[x], v[x].w);
+              at[(s0 + x) * step] = m;
+            }
+        }
       }
+    }
+    __syncthreads();
   }
 }
 

@@ -144,32 +144,37 @@ __device__ __forceinline__ void ssm_sums(const float raw[4], const bool live[4],
 // (block, head), a CTA's eight warps on neighbouring heads, whose dt share sectors.  Made inside
 // the scan by one warp a block this was a chain of 3000 cycles, most of a block's time.
 __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, SsmPrep* prep,
-                                                        int4* items) {
+                                                        int blocks, int4* items, int n_items) {
   grid_dependency_wait();
   grid_launch_dependents();
-  __shared__ int s_ok, s_b;
-  __shared__ long long s_seg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y * 8 + warp;
-  const int seg_blocks = (int)(sp.seg_rows / SB_L);
-  const long long item = blockIdx.x / seg_blocks;
-  const int c = (int)(blockIdx.x % seg_blocks);
-  if (warp == 0) {
+  if ((int)blockIdx.x >= blocks) {  // work items, a warp each
+    const int item = ((int)blockIdx.x - blocks) * 8 + warp;
+    if (blockIdx.y != 0 || item >= n_items) return;
     int b = 0;
     long long seg = 0;
     const bool ok = ssm_find_item(a.seq, item, sp.seg_rows, &b, &seg);
-    if (lane == 0) {
-      s_ok = ok;
-      s_b = b;
-      s_seg = seg;
+    if (lane == 0)
+      items[item] = ok ? make_int4(b, (int)a.seq.start(b), (int)a.seq.end(b),
+                                   (int)(a.seq.start(b) + seg * sp.seg_rows))
+                       : make_int4(-1, 0, 0, 0);
+    return;
+  }
+  if (h >= a.H) return;
+  // the last sequence whose first block is at or before this one
+  int b = 0;
+  if (!a.seq.cu) {
+    b = (int)(blockIdx.x / (unsigned)((a.seq.T + SB_L - 1) / SB_L));
+  } else {
+    int hi = a.seq.B;
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (ssm_first_block(a.seq, mid) <= (long long)blockIdx.x) b = mid; else hi = mid;
     }
   }
-  __syncthreads();
-  const long long seq0 = s_ok ? a.seq.start(s_b) : 0, seq1 = s_ok ? a.seq.end(s_b) : 0;
-  const long long row0 = seq0 + s_seg * sp.seg_rows + (long long)c * SB_L;
-  if (c == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-    items[item] = make_int4(s_ok ? s_b : -1, (int)seq0, (int)seq1, (int)row0);
-  if (!s_ok || h >= a.H) return;
-  if (row0 >= seq1) return;
+  const long long seq0 = a.seq.start(b), seq1 = a.seq.end(b);
+  const long long row0 = seq0 + ((long long)blockIdx.x - ssm_first_block(a.seq, b)) * SB_L;
+  if (row0 < seq0 || row0 >= seq1) return;
   const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
   const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
   float raw[4];
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, S
     out[i] = o.d[i] * exp2f(o.tail[i]);
     w[i] = o.d[i] * exp2f(o.tail[i] + o.later);
   }
-  SsmPrep* pr = prep + (ssm_first_block(a.seq, s_b) + (row0 - seq0) / SB_L) * a.H + h;
+  SsmPrep* pr = prep + (size_t)blockIdx.x * a.H + h;
   reinterpret_cast<float4*>(pr->d)[lane] = make_float4(o.d[0], o.d[1], o.d[2], o.d[3]);
   reinterpret_cast<float4*>(pr->in)[lane] = make_float4(o.in[0], o.in[1], o.in[2], o.in[3]);
   reinterpret_cast<float4*>(pr->out)[lane] = make_float4(out[0], out[1], out[2], out[3]);
@@ -832,43 +837,23 @@ constexpr uint32_t SG_V = SG_K + SG_STAGES * 2 * SB_PANEL;  // stages
 constexpr uint32_t SG_W = SG_V + SG_STAGES * SB_PANEL;      // 4 quarters x 3 parts
 constexpr uint32_t SG_PREP = SG_W + 12 * SB_WPART;          // stages x SsmPrep
 constexpr uint32_t SG_BARS = SG_PREP + SG_STAGES * sizeof(SsmPrep);
-enum { GB_FULL = 0, GB_FREE = 3, GB_WREADY = 6, GB_WFREE = 10, GB_DONE = 14, GB_COUNT };
-constexpr uint32_t SG_TMEM_PTR = SG_BARS + 16 * 8;
+enum { GB_FULL = 0, GB_FREE = 3, GB_WREADY = 6, GB_WFREE = 10, GB_DONE = 14, GB_READ, GB_DRAIN,
+       GB_COUNT };
+constexpr uint32_t SG_TMEM_PTR = SG_BARS + 20 * 8;
 constexpr uint32_t SG_SMEM = SG_TMEM_PTR + 32 + 1024;
 
 __global__ void __launch_bounds__(SG_THREADS, 1)
     ssm_segment_kernel(const __grid_constant__ SsmBlockArgs ba) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_abort, s_item_ok, s_b;
-  __shared__ long long s_seg;
+  __shared__ int s_abort;
   const SsmArgs& a = ba.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const sm = smem_raw + (base - smem_addr(smem_raw));
   const uint32_t bars = base + SG_BARS;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
-
-  const int per_item = a.H * ba.ptiles;
-  const long long item = blockIdx.x / per_item;
-  const int hp = blockIdx.x % per_item, h = hp / ba.ptiles, p0 = hp % ba.ptiles * SB_P;
-  const int g = h / (a.H / a.G);
-  const long long seg_rows = ba.sp.seg_rows;
-  if (warp == 0) {
-    int b = 0;
-    long long s = 0;
-    const bool ok = ssm_find_item(a.seq, item, seg_rows, &b, &s);
-    if (lane == 0) {
-      s_item_ok = ok;
-      s_b = b;
-      s_seg = s;
-      s_abort = 0;
-    }
-  }
-  __syncthreads();
-  if (!s_item_ok) return;
-  const long long row0 = a.seq.start(s_b) + s_seg * seg_rows;
-  if (row0 + seg_rows >= a.seq.end(s_b)) return;  // nothing follows the last segment
-  const int nb = (int)(seg_rows / SB_L);          // all whole
+  if (tid == 0) s_abort = 0;
+  const int nb = (int)(ba.sp.seg_rows / SB_L);  // blocks of a segment that another follows
   const int npanels = a.N > 64 ? 2 : 1;
 
   if (warp == 0) tmem_alloc(base + SG_TMEM_PTR, 128);
@@ -882,6 +867,8 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
       mbar_init(bar(GB_WFREE + i), 1);
     }
     mbar_init(bar(GB_DONE), 1);
+    mbar_init(bar(GB_READ), 4);
+    mbar_init(bar(GB_DRAIN), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (npanels == 1) {
@@ -902,12 +889,28 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
     return reinterpret_cast<const SsmPrep*>(sm + SG_PREP + stage * sizeof(SsmPrep));
   };
 
+  // The pieces of this CTA that a segment follows: each group walks them on its own, `turn` of
+  // them before; their blocks are counted on for the barriers' phases.
+  SsmPiece w;
+  bool ok = true;
+  int piece = (int)blockIdx.x - (int)gridDim.x, turn = -1;
+  auto next_piece = [&]() {
+    for (++turn; ok;) {
+      piece += gridDim.x;
+      if (!ssm_piece(ba, piece, w)) return false;
+      if (w.row1 < w.seq1) return true;
+    }
+    return false;
+  };
+
   if (warp < 8) {
     const int grp = warp >> 2, i0 = tid & 127, rq = i0 >> 2;
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
-    bool ok = true;
+    int stage = 0, round = 0;
+    while (next_piece()) {
+    const int u0 = turn * nb;
     float carry = 0.0f;  // log2 decay of the blocks behind
-    for (int c = 0, stage = 0, round = 0; c < nb && ok; ++c) {
+    for (int c = 0; c < nb && ok; ++c) {
       ok = wait(GB_FULL + stage, round);
       if (!ok) break;
       const uint8_t* vtile = sm + SG_V + stage * SB_PANEL;
@@ -921,7 +924,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
         ssm_parts(*reinterpret_cast<const uint4*>(vtile + 4096 * qd + o0),
                   *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o1),
                   pr.w[32 * qd + rq] * f, p);
-        ok = ok && (c == 0 || wait(GB_WFREE + qd, c - 1));
+        ok = ok && (u0 + c == 0 || wait(GB_WFREE + qd, u0 + c - 1));
         ssm_store_parts(sm + SG_W + qd * 3 * SB_WPART, o0, o1, p);
         fence_async_smem();
         __syncwarp();
@@ -932,13 +935,15 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
         ++round;
       }
     }
-    if (tid == 0 && p0 == 0) ba.sp.decays[item * a.H + h] = exp2f(carry);
-    if (warp < 4 && ok && wait(GB_DONE, 0)) {
+    if (tid == 0 && w.p0 == 0) ba.sp.decays[(size_t)w.item * a.H + w.h] = exp2f(carry);
+    if (warp < 4 && ok) {
+      ok = wait(GB_DONE, turn);
+      if (!ok) break;
       tc_fence_after();
-      const int n = tid, pn = a.P - p0 < SB_P ? a.P - p0 : SB_P;
+      const int n = tid, pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
       const uint32_t lanes = (uint32_t)(warp * 32) << 16;
       // the state before the next segment gets this one's contribution
-      float* to = ba.sp.starts + (((size_t)(item + 1) * a.H + h) * a.N + n) * a.P + p0;
+      float* to = ba.sp.starts + (((size_t)(w.item + 1) * a.H + w.h) * a.N + n) * a.P + w.p0;
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
         float r1[16], r2[16];
@@ -952,59 +957,74 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
                 make_float4(r1[i] + r2[i], r1[i + 1] + r2[i + 1], r1[i + 2] + r2[i + 2],
                             r1[i + 3] + r2[i + 3]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(GB_READ));
+    }
     }
   } else if (warp == 8) {
     constexpr uint32_t dM = mma_desc(128, 128, 1, 1), dM2 = mma_desc(128, 64, 1, 1);
     const uint32_t k0 = tile_desc(base + SG_K, SB_PANEL), w0 = tile_desc(base + SG_W, SB_WPART);
-    bool ok = true;
-    for (int c = 0, stage = 0; c < nb && ok; ++c) {
-      const uint32_t k = k0 + stage * (2 * SB_PANEL >> 4);
-      for (int qd = 0; qd < 4 && ok; ++qd) {
-        ok = wait(GB_WREADY + qd, c);  // the block's tiles are there: its weights were made
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t kq = k + qd * (4096 >> 4), w = w0 + qd * (3 * SB_WPART >> 4);
+    int stage = 0;
+    while (next_piece()) {
+      ok = turn == 0 || wait(GB_READ, turn - 1);  // the sums of the piece before are read
+      for (int c = 0; c < nb && ok; ++c) {
+        const uint32_t k = k0 + stage * (2 * SB_PANEL >> 4);
+        for (int qd = 0; qd < 4 && ok; ++qd) {
+          // the block's tiles are there: its weights were made
+          ok = wait(GB_WREADY + qd, turn * nb + c);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t kq = k + qd * (4096 >> 4), wq = w0 + qd * (3 * SB_WPART >> 4);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mma_ss(tm, kq + i * (2048 >> 4), w + i * (2048 >> 4), dM, c + qd + i > 0);
-            mma_ss(tm, kq + i * (2048 >> 4), w + ((2 * SB_WPART + i * 2048) >> 4), dM2, true);
+            for (int i = 0; i < 2; ++i) {
+              mma_ss(tm, kq + i * (2048 >> 4), wq + i * (2048 >> 4), dM, c + qd + i > 0);
+              mma_ss(tm, kq + i * (2048 >> 4), wq + ((2 * SB_WPART + i * 2048) >> 4), dM2, true);
+            }
+            mma_commit(bar(GB_WFREE + qd));
+            if (qd == 3) mma_commit(bar(GB_FREE + stage));
           }
-          mma_commit(bar(GB_WFREE + qd));
-          if (qd == 3) mma_commit(bar(GB_FREE + stage));
+          __syncwarp();
         }
-        __syncwarp();
+        if (++stage == SG_STAGES) stage = 0;
       }
-      if (++stage == SG_STAGES) stage = 0;
+      if (ok && elect_one()) mma_commit(bar(GB_DONE));
+      __syncwarp();
     }
-    if (elect_one()) mma_commit(bar(GB_DONE));
+    if (elect_one()) mma_commit(bar(GB_DRAIN));
     __syncwarp();
-    mbar_wait(bar(GB_DONE), 0, abort);
+    mbar_wait(bar(GB_DRAIN), 0, abort);
   } else {
-    if (lane == 0) {
-      const SsmPrep* from = ba.prep +
-          (ssm_first_block(a.seq, s_b) + (row0 - a.seq.start(s_b)) / SB_L) * a.H + h;
-      int n = 0;
-      for (int c = 0, stage = 0, round = 0; c < nb; ++c) {
-        const int at = nb - 1 - c, r = (int)(row0 + (long long)at * SB_L);
-        if (c >= SG_STAGES && !wait(GB_FREE + stage, round - 1)) break;
-        mbar_expect(bar(GB_FULL + stage), (npanels + 1) * SB_PANEL + sizeof(SsmPrep));
-        bulk_load(base + SG_PREP + stage * sizeof(SsmPrep), from + (size_t)at * a.H,
-                  sizeof(SsmPrep), bar(GB_FULL + stage));
-        tma_load_3d(base + SG_V + stage * SB_PANEL, &ba.mv, p0, h, r, bar(GB_FULL + stage));
-        for (int pl = 0; pl < npanels; ++pl)
-          tma_load_3d(base + SG_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
-                      bar(GB_FULL + stage));
-        n = c + 1;
-        if (++stage == SG_STAGES) {
-          stage = 0;
-          ++round;
+    int stage = 0, round = 0, n = 0;
+    while (next_piece()) {
+      if (lane == 0) {
+        const SsmPrep* from =
+            ba.prep + (ssm_first_block(a.seq, w.b) + (w.row0 - w.seq0) / SB_L) * a.H + w.h;
+        const int g = w.h / (a.H / a.G);
+        for (int c = 0; c < nb; ++c) {
+          const int at = nb - 1 - c, r = w.row0 + at * SB_L;
+          ok = n < SG_STAGES || wait(GB_FREE + stage, round - 1);
+          if (!ok) break;
+          mbar_expect(bar(GB_FULL + stage), (npanels + 1) * SB_PANEL + sizeof(SsmPrep));
+          bulk_load(base + SG_PREP + stage * sizeof(SsmPrep), from + (size_t)at * a.H,
+                    sizeof(SsmPrep), bar(GB_FULL + stage));
+          tma_load_3d(base + SG_V + stage * SB_PANEL, &ba.mv, w.p0, w.h, r, bar(GB_FULL + stage));
+          for (int pl = 0; pl < npanels; ++pl)
+            tma_load_3d(base + SG_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
+                        bar(GB_FULL + stage));
+          ++n;
+          if (++stage == SG_STAGES) {
+            stage = 0;
+            ++round;
+          }
         }
       }
-      if (*abort)
-        for (int c = n > SG_STAGES ? n - SG_STAGES : 0; c < n; ++c)
-          mbar_wait(bar(GB_FULL + c % SG_STAGES), (uint32_t)(c / SG_STAGES) & 1u, abort);
+      ok = __shfl_sync(FULL_MASK, (int)ok, 0);
     }
+    if (*abort && lane == 0)  // loads in flight land before the memory is given up
+      for (int c = n > SG_STAGES ? n - SG_STAGES : 0; c < n; ++c)
+        mbar_wait(bar(GB_FULL + c % SG_STAGES), (uint32_t)(c / SG_STAGES) & 1u, abort);
   }
   tc_fence_before();
   __syncthreads();
