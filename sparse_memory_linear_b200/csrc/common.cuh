@@ -76,6 +76,14 @@ __device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(gmem) : "memory");
 }
 
+// 16 bytes, or zeros where there is nothing to copy (the source is then not read).
+__device__ __forceinline__ void cp_async16_or_zero(void* smem, const void* gmem, bool copy) {
+  unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem),
+               "r"(copy ? 16 : 0)
+               : "memory");
+}
+
 // Programmatic dependent launch: a grid launched with programmatic stream serialisation
 // can start before the grid ahead of it in the stream has finished.  wait blocks until that
 // grid has completed and its memory is visible (a no-op without the launch attribute);

@@ -95,10 +95,11 @@ struct SsmSplit {
 
 // Token-by-token scan.  A block holds 16 of a head's d_v columns: four per warp, eight lanes to
 // a column, each lane with the state rows 32 j + 4 l .. + 3 in registers.  The chain from token
-// to token is one multiply-add per state value; the sum over the rows ends in three shuffles.
-// Tokens come through shared memory a tile at a time, the tile after next already on its way
-// (cp.async): with a tile loaded only when the one before was done, the loads' latency was
-// nine tenths of the time.  CONTRIB: the first pass of a split (no reads, no y).
+// to token is one multiply-add per state value.  A read's sum over the eight lanes is taken for
+// eight tokens at once, seven shuffles that leave each lane one token's sum (three a token
+// otherwise).  Tokens come through shared memory a tile at a time, the next tile already on its
+// way (cp.async); missing tokens are zeros with a step size of 0, so that the loop has no
+// conditions.  CONTRIB: the first pass of a split (no reads, no y).
 constexpr int SSM_COLS = 16;  // columns of a block
 
 template <typename T>
@@ -186,17 +187,21 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
   auto load = [&](int i) {
     const long long t0 = r0 + (long long)i * TB;
     const int nt = rows_of(i), buf = i & 1, pieces = a.N / E;
-    for (int e = tid; e < nt * pieces; e += 128) {
+    for (int e = tid; e < TB * pieces; e += 128) {
       const int t = e / pieces, c = (e - t * pieces) * E;
-      cp_async16(&sk[buf][t][c], kp + (t0 + t) * a.k_stride + c);
-      if (!CONTRIB) cp_async16(&sq[CONTRIB ? 0 : buf][CONTRIB ? 0 : t][c],
-                               qp + (t0 + t) * a.q_stride + c);
+      const bool in = t < nt;
+      const long long r = in ? t0 + t : t0;
+      cp_async16_or_zero(&sk[buf][t][c], kp + r * a.k_stride + c, in);
+      if (!CONTRIB) cp_async16_or_zero(&sq[CONTRIB ? 0 : buf][CONTRIB ? 0 : t][c],
+                                       qp + r * a.q_stride + c, in);
     }
-    for (int e = tid; e < nt * VC; e += 128) {
+    for (int e = tid; e < TB * VC; e += 128) {
       const int t = e / VC, c = (e - t * VC) * E;
       if (p0 + c >= a.P) continue;
-      cp_async16(&sv[buf][t][c], vp + (t0 + t) * a.v_stride + c);
-      if (!CONTRIB && zp) cp_async16(&sz[buf][t][c], zp + (t0 + t) * a.gate_stride + c);
+      const bool in = t < nt;
+      const long long r = in ? t0 + t : t0;
+      cp_async16_or_zero(&sv[buf][t][c], vp + r * a.v_stride + c, in);
+      if (!CONTRIB && zp) cp_async16_or_zero(&sz[buf][t][c], zp + r * a.gate_stride + c, in);
     }
     cp_async_commit();
   };
@@ -224,32 +229,44 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
       load(i + 1);
       load_dt(i + 1);
     }
-#pragma unroll 4
-    for (int t = 0; t < TB; ++t) {
-      const float al = sa[buf][t], dv = t < nt ? sd[buf][t] * to_f32(sv[buf][t][col]) : 0.0f;
-      float acc = 0.0f;
+#pragma unroll 1
+    for (int t8 = 0; t8 < TB; t8 += 8) {
+      if (t8 >= nt) break;
+      float acc[8];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const float4 k4 = load4_f32(&sk[buf][t][32 * j + 4 * ln]);
-        // a missing token's k may be anything: it must not meet dv
-        if (t < nt) {
+      for (int u = 0; u < 8; ++u) {
+        const int t = t8 + u;
+        const float al = sa[buf][t], dv = sd[buf][t] * to_f32(sv[buf][t][col]);
+        acc[u] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const float4 k4 = load4_f32(&sk[buf][t][32 * j + 4 * ln]);
           s[j][0] = fmaf(s[j][0], al, dv * k4.x);
           s[j][1] = fmaf(s[j][1], al, dv * k4.y);
           s[j][2] = fmaf(s[j][2], al, dv * k4.z);
           s[j][3] = fmaf(s[j][3], al, dv * k4.w);
-        }
-        if (!CONTRIB) {
-          const float4 q4 = load4_f32(&sq[CONTRIB ? 0 : buf][CONTRIB ? 0 : t][32 * j + 4 * ln]);
-          acc = fmaf(q4.x, s[j][0], acc);
-          acc = fmaf(q4.y, s[j][1], acc);
-          acc = fmaf(q4.z, s[j][2], acc);
-          acc = fmaf(q4.w, s[j][3], acc);
+          if (!CONTRIB) {
+            const float4 q4 = load4_f32(&sq[CONTRIB ? 0 : buf][CONTRIB ? 0 : t][32 * j + 4 * ln]);
+            acc[u] = fmaf(q4.x, s[j][0], acc[u]);
+            acc[u] = fmaf(q4.y, s[j][1], acc[u]);
+            acc[u] = fmaf(q4.z, s[j][2], acc[u]);
+            acc[u] = fmaf(q4.w, s[j][3], acc[u]);
+          }
         }
       }
       if (!CONTRIB) {
+        // halves of the tokens go to the lanes with bit 4, 2, 1 set; lane l ends with token l's
 #pragma unroll
-        for (int m = 1; m < 8; m <<= 1) acc += __shfl_xor_sync(FULL_MASK, acc, m);
-        if (ln == 0) sy[buf][t][col] = acc;
+        for (int m = 4; m > 0; m >>= 1) {
+          const bool high = ln & m;
+#pragma unroll
+          for (int u = 0; u < m; ++u) {
+            const float give = high ? acc[u] : acc[u + m];
+            const float keep = high ? acc[u + m] : acc[u];
+            acc[u] = keep + __shfl_xor_sync(FULL_MASK, give, m);
+          }
+        }
+        sy[buf][t8 + ln][col] = acc[0];
       }
     }
     __syncthreads();
