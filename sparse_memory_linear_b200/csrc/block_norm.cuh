@@ -141,12 +141,14 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? (TPR > 256 ? 
       float2 f[4], z[4];
       cur.u[i].get2(f);
       cur.r[i].get2(r[i]);
-      if (a.gate) cur.z[i].get2(z);
+      if (a.gate) {
+        cur.z[i].get2(z);
+        fast_act<4>(z, a.act, z);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float2 t = mul2(mul2(f[e], make_float2(inv, inv)), gpost[e]);
-        if (a.gate)
-          t = mul2(t, make_float2(fast_gate_act(z[e].x, a.act), fast_gate_act(z[e].y, a.act)));
+        if (a.gate) t = mul2(t, z[e]);
         r[i][e] = fma2(t, gscale[e], r[i][e]);
         ss = fmaf(r[i][e].x, r[i][e].x, ss);
         ss = fmaf(r[i][e].y, r[i][e].y, ss);

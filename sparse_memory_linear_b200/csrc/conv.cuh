@@ -189,8 +189,9 @@ struct ConvLane {
       float2 acc = bias[e];
 #pragma unroll
       for (int j = 0; j < K; ++j) acc = fma2(w[j][e], win[j][e], acc);
-      o[e] = make_float2(fast_gate_act(acc.x, act), fast_gate_act(acc.y, act));
+      o[e] = acc;
     }
+    fast_act<2>(o, act, o);
 #pragma unroll
     for (int j = 0; j + 1 < K; ++j)
 #pragma unroll

@@ -11,16 +11,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// act(g) from one exponential and one reciprocal of the hardware, against tens of instructions
-// for expf and a division.  The error relative to act(g) is about 2^-21 (1 + |g| / 4 for negative
-// g): far below half a step of bf16, and a few steps of fp32.
-__device__ __forceinline__ float fast_gate_act(float g, int act) {
-  if (act == SDM_GATE_IDENTITY) return g;
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + fast_exp2(-1.4426950408889634f * g)));
-  return act == SDM_GATE_SILU ? g * r : r;
-}
-
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
@@ -54,6 +44,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// act(g) from one exponential and one reciprocal of the hardware, against tens of instructions
+// for expf and a division.  The error relative to act(g) is about 2^-21 (1 + |g| / 4 for negative
+// g): far below half a step of bf16, and a few steps of fp32.
+// The activation is chosen once for all of a thread's pairs: chosen value by value it cost as
+// much again.
+__device__ __forceinline__ float2 fast_sigmoid2(float2 g) {
+  const float2 t = mul2(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  const float2 d = add2(make_float2(fast_exp2(t.x), fast_exp2(t.y)), make_float2(1.0f, 1.0f));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  return r;
+}
+template <int PAIRS>
+__device__ __forceinline__ void fast_act(const float2 g[PAIRS], int act, float2 out[PAIRS]) {
+  if (act == SDM_GATE_SILU) {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) out[i] = mul2(g[i], fast_sigmoid2(g[i]));
+  } else if (act == SDM_GATE_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) out[i] = fast_sigmoid2(g[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) out[i] = g[i];
+  }
 }
 
 }  // namespace sdm

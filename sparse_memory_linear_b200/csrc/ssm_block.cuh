@@ -476,11 +476,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                            make_float2(y1[2 * j], y1[2 * j + 1])));
         }
         if (zp) {
+          float2 g[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 g = unpack_bf16(z[j]);
-            o[j] = mul2(o[j], make_float2(fast_gate_act(g.x, a.act), fast_gate_act(g.y, a.act)));
-          }
+          for (int j = 0; j < 8; ++j) g[j] = unpack_bf16(z[j]);
+          fast_act<8>(g, a.act, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = mul2(o[j], g[j]);
           if (part < 3) load_z(part + 1);
         }
         uint32_t out[8];
