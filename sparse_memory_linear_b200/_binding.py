@@ -499,21 +499,26 @@ def sdm_state_unpack(codes, scales, d_v: int, fmt: str = "e4m3", *, out=None, st
 _DTYPES = {torch.float32: SDM_F32, torch.bfloat16: SDM_BF16}
 
 
-def _call(name, dev, stream, *args):
-    """Calls the entry point with the stream as its last argument, on the tensors' device: the
-    library launches on the calling thread's current one."""
+def _scope(stream, dev):
+    """The given stream (a torch stream or a raw handle) as the current one of the tensors' device:
+    what a call allocates then belongs to the stream that it runs on."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _call(name, dev, *args):
+    """Calls the entry point with the device's current stream as its last argument, on the
+    tensors' device: the library launches on the calling thread's current one."""
     fn = getattr(_lib or library(), name)
     index = dev.index
-    if stream is None:
-        # the raw handle: a Stream object costs as much as the launch
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
+    # the raw handle: a Stream object costs as much as the launch
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
-        rc = fn(*args, int(stream))
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, int(stream))
+            rc = fn(*args, stream)
     if rc != 0:
         raise SdmError(rc, name)
 
@@ -616,6 +621,9 @@ def sdm_conv_forward(x, w, state=None, *, bias=None, init: str = "zero", act: st
     [B+1]; rows may be pitched).  w [C,K] fp32, K = 2 to 4, bias [C] fp32; state [B,K-1,C]
     (a sequence's last K-1 inputs) is read with init="continue" and rewritten.  Returns y."""
     dev, dt = _cuda(x, "x")
+    if stream is not None:
+        with _scope(stream, dev):
+            return sdm_conv_forward(x, w, state, bias=bias, init=init, act=act, cu=cu, y=y)
     B, T = _batch(cu, tuple(x.shape[:-1]), dev)
     C = x.shape[-1]
     if w.dim() != 2:
@@ -624,7 +632,7 @@ def sdm_conv_forward(x, w, state=None, *, bias=None, init: str = "zero", act: st
     pitch = _pitch(x, "x", x.shape, x.dim() - 1, dt, dev)
     y = _out(y, x, pitch, dt)
     _like(state, "state", (B, K - 1, C), dt, dev)
-    _call("sdm_conv_forward", dev, stream, x.data_ptr(), _param(w, "w", (C, K), dev),
+    _call("sdm_conv_forward", dev, x.data_ptr(), _param(w, "w", (C, K), dev),
           _param(bias, "bias", (C,), dev), _addr(state), _dense_init(init), ACT[act], _addr(cu),
           y.data_ptr(), SdmConvShape(B, T, C, K, _DTYPES[dt], pitch))
     return y
@@ -634,6 +642,9 @@ def sdm_conv_step(x, w, state, *, bias=None, act: str = "silu", y=None, stream=N
     """One token of each sequence: x [B,C] (rows may be pitched), w [C,K] fp32, bias [C] fp32;
     state [B,K-1,C] is read and moved up by one.  Returns y [B,C]."""
     dev, dt = _cuda(x, "x")
+    if stream is not None:
+        with _scope(stream, dev):
+            return sdm_conv_step(x, w, state, bias=bias, act=act, y=y)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError(f"x and w must be [B, C] and [C, K], got {tuple(x.shape)} and "
                          f"{tuple(w.shape)}")
@@ -641,8 +652,10 @@ def sdm_conv_step(x, w, state, *, bias=None, act: str = "silu", y=None, stream=N
     K = w.shape[1]
     pitch = _pitch(x, "x", x.shape, 1, dt, dev)
     y = _out(y, x, pitch, dt)
+    if state is None:
+        raise ValueError("a step needs the state of the tokens before")
     _like(state, "state", (B, K - 1, C), dt, dev)
-    _call("sdm_conv_step", dev, stream, x.data_ptr(), _param(w, "w", (C, K), dev),
+    _call("sdm_conv_step", dev, x.data_ptr(), _param(w, "w", (C, K), dev),
           _param(bias, "bias", (C,), dev), state.data_ptr(), ACT[act], y.data_ptr(),
           SdmConvShape(B, 1, C, K, _DTYPES[dt], pitch))
     return y
@@ -686,6 +699,10 @@ def sdm_ssm_forward(k, q, v, dt, A, M, *, init: str = "zero", D=None, dt_bias=No
     row); A [H] fp32 (<= 0), D, dt_bias [H] fp32; M [B,H,N,d_v] fp32, read with
     init="continue" and left as it is after the last token.  Returns y like v."""
     dev, dtype = _cuda(v, "v")
+    if stream is not None:
+        with _scope(stream, dev):
+            return sdm_ssm_forward(k, q, v, dt, A, M, init=init, D=D, dt_bias=dt_bias,
+                                   softplus=softplus, gate=gate, act=act, cu=cu, y=y, ws=ws)
     if v.dim() < 3 or k.dim() != v.dim():
         raise ValueError(f"k and v must be [..., G, N] and [..., H, d_v] rows, got "
                          f"{tuple(k.shape)} and {tuple(v.shape)}")
@@ -698,7 +715,7 @@ def sdm_ssm_forward(k, q, v, dt, A, M, *, init: str = "zero", D=None, dt_bias=No
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     else:
         _need(ws, "ws", torch.uint8, dev)
-    _call("sdm_ssm_forward", dev, stream, k.data_ptr(), q.data_ptr(), v.data_ptr(),
+    _call("sdm_ssm_forward", dev, k.data_ptr(), q.data_ptr(), v.data_ptr(),
           dt.data_ptr(), *params, M.data_ptr(), _dense_init(init), _addr(gate), ACT[act],
           _addr(cu), y.data_ptr(), _addr(ws), ws.numel() if ws is not None else 0, shape)
     return y
@@ -709,12 +726,16 @@ def sdm_ssm_step(k, q, v, dt, A, M, *, D=None, dt_bias=None, softplus: bool = Tr
     """One token of each sequence: k, q [B,G,N], v, gate [B,H,d_v], dt [B,H]; M [B,H,N,d_v]
     fp32 is read and rewritten.  Returns y [B,H,d_v]."""
     dev, dtype = _cuda(v, "v")
+    if stream is not None:
+        with _scope(stream, dev):
+            return sdm_ssm_step(k, q, v, dt, A, M, D=D, dt_bias=dt_bias, softplus=softplus,
+                                gate=gate, act=act, y=y)
     if v.dim() != 3 or k.dim() != 3:
         raise ValueError(f"k and v must be [B, G, N] and [B, H, d_v], got {tuple(k.shape)} and "
                          f"{tuple(v.shape)}")
     shape, y, params = _ssm_shape(k, q, v, dt, A, M, D, dt_bias, gate, y, softplus, v.shape[0],
                                   1, dev, dtype)
-    _call("sdm_ssm_step", dev, stream, k.data_ptr(), q.data_ptr(), v.data_ptr(), dt.data_ptr(),
+    _call("sdm_ssm_step", dev, k.data_ptr(), q.data_ptr(), v.data_ptr(), dt.data_ptr(),
           *params, M.data_ptr(), _addr(gate), ACT[act], y.data_ptr(), shape)
     return y
 
@@ -727,6 +748,11 @@ def sdm_block_norm(u, r, *, post_norm: bool = True, post_gamma=None, gate=None,
     the residual stream (bf16 or fp32); post_gamma, scale, pre_gamma [D] fp32.  r_out may be
     r, n may be u or gate.  want_n=False: the second result is None."""
     dev, dtype = _cuda(u, "u")
+    if stream is not None:
+        with _scope(stream, dev):
+            return sdm_block_norm(u, r, post_norm=post_norm, post_gamma=post_gamma, gate=gate,
+                                  act=act, scale=scale, pre_gamma=pre_gamma, eps=eps,
+                                  r_out=r_out, n=n, want_n=want_n)
     _, rdt = _cuda(r, "r")
     D = u.shape[-1]
     _like(u, "u", u.shape, dtype, dev)
@@ -740,7 +766,7 @@ def sdm_block_norm(u, r, *, post_norm: bool = True, post_gamma=None, gate=None,
         n = torch.empty_like(u) if want_n else None
     else:
         _like(n, "n", u.shape, dtype, dev)
-    _call("sdm_block_norm", dev, stream, u.data_ptr(), _addr(gate), ACT[act],
+    _call("sdm_block_norm", dev, u.data_ptr(), _addr(gate), ACT[act],
           1 if post_norm else 0, _param(post_gamma, "post_gamma", (D,), dev),
           _param(scale, "scale", (D,), dev), r.data_ptr(), _DTYPES[rdt],
           _param(pre_gamma, "pre_gamma", (D,), dev), eps, r_out.data_ptr(), _addr(n),

@@ -283,7 +283,7 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
 }
 
 SsmSplit ssm_split(const SsmPlan& plan, void* ws) {
-  return SsmSplit{plan.seg_rows, static_cast<float*>(ws),
+  return SsmSplit{plan.seg_rows, plan.items, static_cast<float*>(ws),
                   reinterpret_cast<float*>(static_cast<char*>(ws) + plan.off_decays)};
 }
 

@@ -89,6 +89,7 @@ __device__ __forceinline__ bool ssm_find_item(const SeqBounds& seq, long long it
 // segments turns those into the states before them, and the scan starts from these.
 struct SsmSplit {
   long long seg_rows;  // rows of a segment
+  long long items;     // places for segments' states; only bad offsets ask for more
   float* starts;       // [items, H, N, P]: the state before each segment of a split sequence
   float* decays;       // [items, H]: the segment's whole decay
 };
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
   const long long seq0 = a.seq.start(b), seq1 = a.seq.end(b), r0 = seq0 + s_seg * sp.seg_rows;
   const long long r1 = r0 + sp.seg_rows < seq1 ? r0 + sp.seg_rows : seq1;
   const bool split = seq1 - seq0 > sp.seg_rows;
-  if (CONTRIB && r1 == seq1) return;  // nothing follows the last segment
+  // nothing follows the last segment; no place for what bad offsets make up
+  if (CONTRIB && (r1 == seq1 || blockIdx.x + 1 >= sp.items)) return;
   const T* kp = static_cast<const T*>(a.k) + (size_t)g * a.N;
   const T* qp = static_cast<const T*>(a.q) + (size_t)g * a.N;
   const T* vp = static_cast<const T*>(a.v) + (size_t)h * a.P + p0;
@@ -333,8 +335,9 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) 
         if (items) atomicAdd(&s_first, items);
       }
       __syncthreads();
-      const long long first = (long long)s_first;
-      const int segs = (int)items_of(b);
+      const long long first = (long long)s_first, room = sp.items - first;
+      const int segs = (int)(items_of(b) < room ? items_of(b) : room);
+      if (segs <= 0) continue;
       for (int unit = blockIdx.x; unit < a.H * parts; unit += gridDim.x) {
         const int h = unit / parts, i = (unit - h * parts) * 256 + (int)threadIdx.x;
         if (i >= n4) continue;

@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
     for (++turn; ok;) {
       piece += gridDim.x;
       if (!ssm_piece(ba, piece, w)) return false;
-      if (w.row1 < w.seq1) return true;
+      if (w.row1 < w.seq1 && w.item + 1 < ba.sp.items) return true;
     }
     return false;
   };

@@ -355,6 +355,26 @@ def test_ssm_bad_offsets_are_reported(sdm):
             assert (y[20:] == 7).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [1, 64])
+def test_ssm_bad_offsets_of_long_sequences(sdm, dt, H):
+    """Offsets that make up more rows than there are, in a batch that is cut into segments: every
+    access stays in the buffers (canaries around scratch, state and y), and it is reported."""
+    T, B, N, P = 3000, 6, 64, 64
+    i, _ = ssm_inputs(gen(8), (T,), H, 1, N, P, TYPES[dt], False, False, B)
+    for cu in ([0, T, 0, T, 0, T, 0], [0, 2 * T, -5, T, 7, T, T], [T, 0, T, 0, T, 0, T]):
+        c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        shape = sdm.SdmSsmShape(B, T, H, 1, N, P, 1 if dt == "bf16" else 0, 1, 0, 0, 0, 0, 0)
+        need = sdm.sdm_ssm_workspace_size(shape)
+        big = torch.full((need + (1 << 22),), 0x5a, dtype=torch.uint8, device=DEV)
+        M = torch.full((B + 2, H, N, P), 3.0, device=DEV)
+        y = torch.full((T + 256, H, P), 7.0, dtype=TYPES[dt], device=DEV)
+        sdm.sdm_ssm_forward(M=M[1:-1], cu=c, y=y[128:-128], ws=big[:need] if need else None, **i)
+        assert sdm.sdm_get_device_status() == 4
+        assert (big[need:] == 0x5a).all() and (M[0] == 3).all() and (M[-1] == 3).all()
+        assert (y[:128] == 7).all() and (y[-128:] == 7).all()
+
+
 # ------------------------------------------------------------------------------- block norm
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("res", ["bf16", "f32"])
@@ -507,6 +527,23 @@ def test_layer_in_graphs_and_streams(sdm):
         got = layer(sdm, p, x, r, csb, Mb)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(Mb, M)
+
+    # the same by a stream argument, a torch stream's and a raw handle
+    for handle in (side, side.cuda_stream):
+        csb, Mb = fresh()
+        side.wait_stream(torch.cuda.current_stream())
+        row = sdm.sdm_conv_forward(x["row"], p["w"], csb, bias=p["bias"], stream=handle)
+        side.synchronize()
+        assert torch.equal(csb, cs)
+        H, G, N, P = p["H"], p["G"], p["N"], p["P"]
+        v, k, q = row.split([H * P, G * N, G * N], -1)
+        y = sdm.sdm_ssm_forward(k.unflatten(-1, (G, N)), q.unflatten(-1, (G, N)),
+                                v.unflatten(-1, (H, P)), x["dt"], p["A"], Mb, D=p["D"],
+                                dt_bias=p["dt_bias"], gate=x["gate"], stream=handle)
+        out = sdm.sdm_block_norm(y.flatten(-2), r, post_gamma=p["pg"], scale=p["sc"],
+                                 pre_gamma=p["qg"], stream=handle)
+        side.synchronize()
+        assert torch.equal(Mb, M) and all(torch.equal(a, b) for a, b in zip(out, want))
 
     graphs, outs, states = [], [], []
     xs = [{k: torch.zeros_like(v) for k, v in d.items()} for d in (x, one)]
