@@ -6,6 +6,10 @@
 //   r' = r + f
 //   n = r' * rsqrt(mean(r'^2) + eps) * pre_gamma     (the next block's input)
 // Both means and the sum are fp32; n is computed from the unrounded r'.
+//
+// Bound by its bytes: 32768 rows of 2048, bf16 with a gate and an fp32 residual (14 bytes a value),
+// take 161 us, 5.84 TB/s, 0.89 of the measured copy rate.  A first version that read the
+// parameters for every row and waited for each row's values took 206 us.
 #pragma once
 
 #include "common.cuh"
@@ -143,7 +147,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? (TPR > 256 ? 
       cur.r[i].get2(r[i]);
       if (a.gate) {
         cur.z[i].get2(z);
-        fast_act<4>(z, a.act, z);
+        fast_act<4>(z, a.act);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

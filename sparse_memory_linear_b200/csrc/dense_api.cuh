@@ -350,8 +350,9 @@ sdm_status ssm_block_run(const sdm_ssm_shape& s, const SsmArgs& a, const DeviceI
     return SDM_ERR_CUDA;
   const long long blocks = plan.items * s.H * ba.ptiles;
   if (blocks > 2147483647LL) return SDM_ERR_UNSUPPORTED;
-  ba.pieces = (int)blocks;
   const unsigned ctas = (unsigned)(blocks < di->sms ? blocks : di->sms);
+  ba.step_items = (int)ctas / (s.H * ba.ptiles);
+  ba.step_parts = (int)ctas % (s.H * ba.ptiles);
   const long long preps = ssm_prep_blocks(s, a.seq.cu != nullptr);
   SDM_CUDA_TRY(launch_pdl<true>(ssm_prep_kernel,
                                 dim3((unsigned)(preps + (plan.items + 7) / 8),

@@ -60,16 +60,13 @@ __device__ __forceinline__ float2 fast_sigmoid2(float2 g) {
   return r;
 }
 template <int PAIRS>
-__device__ __forceinline__ void fast_act(const float2 g[PAIRS], int act, float2 out[PAIRS]) {
-  if (act == SDM_GATE_SILU) {
+__device__ __forceinline__ void fast_act(float2 g[PAIRS], int act) {
+  if (act == SDM_GATE_IDENTITY) return;
+  const bool silu = act == SDM_GATE_SILU;
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) out[i] = mul2(g[i], fast_sigmoid2(g[i]));
-  } else if (act == SDM_GATE_SIGMOID) {
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) out[i] = fast_sigmoid2(g[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) out[i] = g[i];
+  for (int i = 0; i < PAIRS; ++i) {
+    const float2 s = fast_sigmoid2(g[i]);
+    g[i] = mul2(s, make_float2(silu ? g[i].x : 1.0f, silu ? g[i].y : 1.0f));
   }
 }
 

@@ -85,7 +85,7 @@ struct SsmBlockArgs {
   SsmPrep* prep;    // [blocks, H]
   int4* items;      // [items] (sequence, its first and past-last row, the segment's first row)
   int ptiles;       // 64-column tiles of d_v
-  int pieces;       // items x H x ptiles
+  int step_items, step_parts;  // gridDim.x = step_items x (H x ptiles) + step_parts
 };
 
 // The place of a sequence's first block among all blocks' sums: sequences of T rows one after
@@ -202,19 +202,28 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, S
     pr->run[lane] = lane == 0 ? o.run[0] : lane == 1 ? o.run[1] : lane == 2 ? o.run[2] : o.run[3];
 }
 
-// Eight pairs of values times w, in three bf16 parts.
+// Eight pairs of values times w, in three bf16 parts that add up to the fp32 products exactly:
+// each part is the next eight bits of what is left (cut, not rounded: the upper half of the word
+// as it stands, two fewer instructions a pair than a conversion and its way back).
 __device__ __forceinline__ void ssm_parts(const uint4& va, const uint4& vb, float w,
                                           uint32_t p[3][8]) {
   const float2 w2 = make_float2(w, w);
   const uint32_t vw[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+  auto upper = [](float2 x) {  // the upper halves of both words
+    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+  };
+  auto rest = [](float2 x) {
+    return sub2(x, make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                               __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)));
+  };
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     float2 x = mul2(unpack_bf16(vw[j]), w2);
-    p[0][j] = pack_bf16(x.x, x.y);
-    x = sub2(x, unpack_bf16(p[0][j]));
-    p[1][j] = pack_bf16(x.x, x.y);
-    x = sub2(x, unpack_bf16(p[1][j]));
-    p[2][j] = pack_bf16(x.x, x.y);
+    p[0][j] = upper(x);
+    x = rest(x);
+    p[1][j] = upper(x);
+    x = rest(x);
+    p[2][j] = upper(x);
   }
 }
 __device__ __forceinline__ void ssm_store_parts(uint8_t* place, uint32_t o0, uint32_t o1,
@@ -228,34 +237,50 @@ __device__ __forceinline__ void ssm_store_parts(uint8_t* place, uint32_t o0, uin
   }
 }
 
-// One piece of the scan's work: a segment of a sequence, a head and 64 of its columns.
+// One piece of the scan's work: a segment of a sequence, a head and 64 of its columns.  A CTA
+// walks every gridDim.x-th piece.
 struct SsmPiece {
-  int item, b, seq0, seq1, row0, row1, h, p0, nb;  // nb blocks
+  int item, part;  // work item, and its part: head + H x tile
+  int b, seq0, seq1, row0, row1, h, p0, nb;  // nb blocks
+  __device__ __forceinline__ void begin(const SsmBlockArgs& ba) {
+    const int parts = ba.a.H * ba.ptiles;
+    item = (int)blockIdx.x / parts;
+    part = (int)blockIdx.x - item * parts;
+  }
+  // The piece at hand; false past the last.
+  __device__ __forceinline__ bool get(const SsmBlockArgs& ba) {
+    if (item >= ba.sp.items) return false;
+    const int4 at = __ldg(ba.items + item);
+    const int H = ba.a.H;
+    h = part;
+    p0 = 0;
+    while (h >= H) {  // at most three times: d_v <= 256
+      h -= H;
+      p0 += SB_P;
+    }
+    b = at.x;
+    seq0 = at.y;
+    seq1 = at.z;
+    row0 = at.w;
+    const int left = seq1 - row0, most = (int)ba.sp.seg_rows;
+    row1 = row0 + (left < most ? left : most);
+    nb = (row1 - row0 + SB_L - 1) / SB_L;
+    return b >= 0;
+  }
+  __device__ __forceinline__ void advance(const SsmBlockArgs& ba) {
+    item += ba.step_items;
+    part += ba.step_parts;
+    const int parts = ba.a.H * ba.ptiles;
+    if (part >= parts) {
+      part -= parts;
+      ++item;
+    }
+  }
 };
-// False past the last.
-__device__ __forceinline__ bool ssm_piece(const SsmBlockArgs& ba, int i, SsmPiece& w) {
-  if (i >= ba.pieces) return false;
-  const int per_item = ba.a.H * ba.ptiles;
-  w.item = i / per_item;
-  const int hp = i - w.item * per_item;
-  w.h = hp / ba.ptiles;
-  w.p0 = (hp - w.h * ba.ptiles) * SB_P;
-  const int4 at = __ldg(ba.items + w.item);
-  if (at.x < 0) return false;
-  w.b = at.x;
-  w.seq0 = at.y;
-  w.seq1 = at.z;
-  w.row0 = at.w;
-  const int left = w.seq1 - w.row0;
-  w.row1 = w.row0 + (left < ba.sp.seg_rows ? left : (int)ba.sp.seg_rows);
-  w.nb = (w.row1 - w.row0 + SB_L - 1) / SB_L;
-  return true;
-}
 
 __global__ void __launch_bounds__(SB_THREADS, 1)
     ssm_block_kernel(const __grid_constant__ SsmBlockArgs ba) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_abort;
   const SsmArgs& a = ba.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -263,7 +288,6 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   const uint32_t bars = base + SB_BARS;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   if (blockIdx.x == 0) a.seq.check();
-  if (tid == 0) s_abort = 0;
   const int npanels = a.N > 64 ? 2 : 1, nk = (a.N + 15) / 16;
 
   if (warp == 0) tmem_alloc(base + SB_TMEM_PTR, 512);
@@ -306,9 +330,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + SB_TMEM_PTR);
-  volatile int* const abort = &s_abort;
   // use: how many times the barrier completed before
-  auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u, abort); };
+  auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u); };
   auto prep = [&](int c) {
     return reinterpret_cast<SsmPrep*>(sm + SB_PREP + (c & 3) * sizeof(SsmPrep));
   };
@@ -319,13 +342,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   SsmPiece w;
   bool ok = true;
   int u0 = 0;
-  auto next_piece = [&](int i) { return ok && ssm_piece(ba, i, w); };
+  w.begin(ba);
 
   if (warp < 4) {
     // ------------------------------------------------ P: row t = tid
     const int t = tid;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
     for (int c = u0; c < u0 + w.nb; ++c) {
       const uint32_t stage = c & 1;
       ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_S + stage, c >> 1);
@@ -412,7 +435,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     // ------------------------------------------------ Y: row t = tid - 128
     const int t = tid - 128, quad = warp - 4;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    for (; ok && w.get(ba); u0 += w.nb, w.advance(ba)) {
     const float D = a.D ? a.D[w.h] : 0.0f;
     const float2 D2 = make_float2(D, D);
     const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;  // columns that exist
@@ -479,7 +502,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           float2 g[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) g[j] = unpack_bf16(z[j]);
-          fast_act<8>(g, a.act, g);
+          fast_act<8>(g, a.act);
 #pragma unroll
           for (int j = 0; j < 8; ++j) o[j] = mul2(o[j], g[j]);
           if (part < 3) load_z(part + 1);
@@ -531,7 +554,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_HREADY));
     };
-    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    for (; ok && w.get(ba); u0 += w.nb, w.advance(ba)) {
     const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
     float* const mrow = a.M + (((size_t)w.b * a.H + w.h) * a.N + n) * a.P + w.p0;
     const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
@@ -597,7 +620,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     // ------------------------------------------------ W: three bf16 parts of w o v
     const int i0 = tid - 384, rq = i0 >> 2;  // row in the quarter, and 16 of its values
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
-    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
     for (int c = u0; c < u0 + w.nb; ++c) {
       const int stage = c & 1;
       ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
@@ -649,7 +672,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY2 = mma_desc(128, 64, 0, 1);
     const uint32_t q0 = tile_desc(base + SB_Q), k0 = tile_desc(base + SB_K),
                    h0 = tile_desc(base + SB_H);
-    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
     for (int c = u0 - 1; c < u0 + w.nb; ++c) {
       if (c >= u0) {
         const uint32_t stage = c & 1;
@@ -693,13 +716,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     }
     if (elect_one()) mma_commit(bar(BAR_DRAIN));
     __syncwarp();
-    mbar_wait(bar(BAR_DRAIN), 0, abort);
+    ok = mbar_wait(bar(BAR_DRAIN), 0) && ok;
   } else if (warp == 17) {
     // ------------------------------------------------ products dM, part onto part, and Y1
     constexpr uint32_t dM = mma_desc(128, 64, 1, 1), dY1 = mma_desc(128, 64, 0, 1);
     const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W),
                    v0 = tile_desc(base + SB_V);
-    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb)
+    for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
     for (int c = u0; c < u0 + w.nb && ok; ++c) {
       const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
       ok = wait(BAR_KFULL + stage, c >> 1) &&
@@ -727,8 +750,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       ok = ok && wait(BAR_VFULL + (c & 3), c >> 2) && wait(BAR_P + stage, c >> 1);
       if (!ok) break;
       tc_fence_after();
+      const uint32_t slot = c & 3;
       if (elect_one()) {
-        const uint32_t v = v0 + (c & 3) * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
+        const uint32_t v = v0 + slot * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
 #pragma unroll
         for (int i = 0; i < SB_L / 16; ++i)
           mma_ts(s + TM_Y1, s + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
@@ -738,11 +762,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     }
     if (elect_one()) mma_commit(bar(BAR_DRAIN + 1));
     __syncwarp();
-    mbar_wait(bar(BAR_DRAIN + 1), 0, abort);
+    ok = mbar_wait(bar(BAR_DRAIN + 1), 0) && ok;
   } else if (warp == 19) {
     // ------------------------------------------------ loads of k and q
     int kc = 0, qc = 0;  // blocks whose load is issued
-    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    for (; ok && w.get(ba); u0 += w.nb, w.advance(ba)) {
       if (lane == 0) {
         const int g = w.h / (a.H / a.G);
         for (int c = u0; c < u0 + w.nb; ++c) {
@@ -765,16 +789,16 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
       ok = __shfl_sync(FULL_MASK, (int)ok, 0);
     }
-    if (*abort && lane == 0) {
+    if (!ok && lane == 0) {
       // loads in flight land before the block's memory is given up (each wait limited)
-      if (qc) mbar_wait(bar(BAR_QFULL), (uint32_t)(qc - 1) & 1u, abort);
+      if (qc) mbar_wait(bar(BAR_QFULL), (uint32_t)(qc - 1) & 1u);
       for (int c = kc > 2 ? kc - 2 : 0; c < kc; ++c)
-        mbar_wait(bar(BAR_KFULL + (c & 1)), (uint32_t)(c >> 1) & 1u, abort);
+        mbar_wait(bar(BAR_KFULL + (c & 1)), (uint32_t)(c >> 1) & 1u);
     }
   } else {
     // ------------------------------------------------ loads of v and the blocks' sums
     int pc = 0, vc = 0;  // blocks whose load is issued
-    for (int piece = blockIdx.x; next_piece(piece); piece += gridDim.x, u0 += w.nb) {
+    for (; ok && w.get(ba); u0 += w.nb, w.advance(ba)) {
       // what groups H and Y read on their own comes into the L2 ahead of them: the state before
       // the piece, and block by block the gate
       const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
@@ -808,11 +832,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
       ok = __shfl_sync(FULL_MASK, (int)ok, 0);
     }
-    if (*abort && lane == 0) {
+    if (!ok && lane == 0) {
       for (int c = pc > 4 ? pc - 4 : 0; c < pc; ++c)
-        mbar_wait(bar(BAR_PREP + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
+        mbar_wait(bar(BAR_PREP + (c & 3)), (uint32_t)(c >> 2) & 1u);
       for (int c = vc > 4 ? vc - 4 : 0; c < vc; ++c)
-        mbar_wait(bar(BAR_VFULL + (c & 3)), (uint32_t)(c >> 2) & 1u, abort);
+        mbar_wait(bar(BAR_VFULL + (c & 3)), (uint32_t)(c >> 2) & 1u);
     }
   }
   }
@@ -820,6 +844,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_free(tm, 512);
+  if (!ok) record_status(STATUS_TIMEOUT);
 }
 
 // ------------------------------------------------------------------------ split sequences
@@ -846,14 +871,12 @@ constexpr uint32_t SG_SMEM = SG_TMEM_PTR + 32 + 1024;
 __global__ void __launch_bounds__(SG_THREADS, 1)
     ssm_segment_kernel(const __grid_constant__ SsmBlockArgs ba) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_abort;
   const SsmArgs& a = ba.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const sm = smem_raw + (base - smem_addr(smem_raw));
   const uint32_t bars = base + SG_BARS;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
-  if (tid == 0) s_abort = 0;
   const int nb = (int)(ba.sp.seg_rows / SB_L);  // blocks of a segment that another follows
   const int npanels = a.N > 64 ? 2 : 1;
 
@@ -884,8 +907,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + SG_TMEM_PTR);
-  volatile int* const abort = &s_abort;
-  auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u, abort); };
+  auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u); };
   auto prep = [&](int stage) {
     return reinterpret_cast<const SsmPrep*>(sm + SG_PREP + stage * sizeof(SsmPrep));
   };
@@ -894,13 +916,13 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
   // them before; their blocks are counted on for the barriers' phases.
   SsmPiece w;
   bool ok = true;
-  int piece = (int)blockIdx.x - (int)gridDim.x, turn = -1;
+  int turn = -1;
+  w.begin(ba);
   auto next_piece = [&]() {
-    for (++turn; ok;) {
-      piece += gridDim.x;
-      if (!ssm_piece(ba, piece, w)) return false;
+    if (turn >= 0) w.advance(ba);
+    ++turn;
+    for (; ok && w.get(ba); w.advance(ba))
       if (w.row1 < w.seq1 && w.item + 1 < ba.sp.items) return true;
-    }
     return false;
   };
 
@@ -995,7 +1017,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
     }
     if (elect_one()) mma_commit(bar(GB_DRAIN));
     __syncwarp();
-    mbar_wait(bar(GB_DRAIN), 0, abort);
+    ok = mbar_wait(bar(GB_DRAIN), 0) && ok;
   } else {
     int stage = 0, round = 0, n = 0;
     while (next_piece()) {
@@ -1023,14 +1045,15 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
       }
       ok = __shfl_sync(FULL_MASK, (int)ok, 0);
     }
-    if (*abort && lane == 0)  // loads in flight land before the memory is given up
+    if (!ok && lane == 0)  // loads in flight land before the memory is given up
       for (int c = n > SG_STAGES ? n - SG_STAGES : 0; c < n; ++c)
-        mbar_wait(bar(GB_FULL + c % SG_STAGES), (uint32_t)(c / SG_STAGES) & 1u, abort);
+        mbar_wait(bar(GB_FULL + c % SG_STAGES), (uint32_t)(c / SG_STAGES) & 1u);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_free(tm, 128);
+  if (!ok) record_status(STATUS_TIMEOUT);
 }
 
 }  // namespace sdm

@@ -22,30 +22,11 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// Whether the phase is over, without waiting for it.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Every wait ends: a try suspends the thread for up to two microseconds, and after 2^20 of them
-// (seconds, against microseconds in a sound run) the wait gives up, raises the block's abort flag
-// and records SDM_ERR_TIMEOUT; the caller leaves its loop, and the block's other waits run out in
-// the same way.  No call in here: one would cost the callers their registers.
-constexpr unsigned long long MBAR_LIMIT_NS = 2000000000ull;
-__device__ __forceinline__ unsigned long long wall_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+// (seconds, against microseconds in a sound run) the wait gives up and the caller leaves its
+// loops; the block's other waits run out in the same way, and the kernel records SDM_ERR_TIMEOUT
+// when it ends.  Kept to a few instructions: a kernel has dozens of these.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
@@ -61,10 +42,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
-  if (ok) return true;
-  *abort = 1;
-  record_status(STATUS_TIMEOUT);
-  return false;
+  return ok != 0;
 }
 
 // This thread's writes to shared memory become visible to the TMA and the matrix unit.
