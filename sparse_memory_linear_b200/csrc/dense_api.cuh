@@ -278,7 +278,7 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
   const long long blocks = ssm_prep_blocks(s, packed);
   p.off_prep = p.bytes;
   p.off_items = p.bytes + round_up((size_t)blocks * s.H * sizeof(SsmPrep), WS_ALIGN);
-  p.bytes = p.off_items + round_up((size_t)p.items * sizeof(int4), WS_ALIGN);
+  p.bytes = p.off_items + round_up((size_t)p.items * (sizeof(int4) + sizeof(int)), WS_ALIGN);
   return p;
 }
 

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
 
 // The states before the segments of a split sequence, from the first on: what the sequence
 // starts with, then each segment's decay and contribution.  Blocks share the (head, 1024 state
-// values) parts of every split sequence; the sequences are looked through 256 at a time, so
+// values) units of all split sequences; the sequences are looked through 256 at a time, so
 // that a batch of short ones costs next to nothing.  Eight segments' values are on their way at
 // a time.
 __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) {
@@ -318,6 +318,8 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) 
     const long long len = a.seq.end(b) - a.seq.start(b);
     return len > 0 ? (len + seg - 1) / seg : 1;
   };
+  const int units = a.H * parts, grid = (int)gridDim.x;
+  int ahead = 0;  // the split sequences' units before this one, modulo the blocks
   for (int b0 = 0; b0 < a.seq.B; b0 += 256) {
     const int e = b0 + (int)threadIdx.x;
     const int mine = e < a.seq.B && a.seq.end(e) - a.seq.start(e) > seg;
@@ -325,7 +327,9 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) 
     if (!__syncthreads_or(mine)) continue;
     for (int j = 0; j < 256 && b0 + j < a.seq.B; ++j) {
       if (!s_split[j]) continue;
-      const int b = b0 + j;
+      const int b = b0 + j, mine0 = ((int)blockIdx.x + grid - ahead) % grid;
+      ahead = (ahead + units) % grid;
+      if (mine0 >= units) continue;
       __syncthreads();
       if (threadIdx.x == 0) s_first = a.seq.cu ? 0 : b * items_of(b);
       __syncthreads();
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) 
       const long long first = (long long)s_first, room = sp.items - first;
       const int segs = (int)(items_of(b) < room ? items_of(b) : room);
       if (segs <= 0) continue;
-      for (int unit = blockIdx.x; unit < a.H * parts; unit += gridDim.x) {
+      for (int unit = mine0; unit < units; unit += grid) {
         const int h = unit / parts, i = (unit - h * parts) * 256 + (int)threadIdx.x;
         if (i >= n4) continue;
         float4* at = reinterpret_cast<float4*>(sp.starts) + ((size_t)first * a.H + h) * n4 + i;

@@ -83,7 +83,8 @@ struct SsmBlockArgs {
   CUtensorMap mq, mk, mv, mz;  // mz: the gate, where there is one
   SsmSplit sp;      // segments of whole blocks
   SsmPrep* prep;    // [blocks, H]
-  int4* items;      // [items] (sequence, its first and past-last row, the segment's first row)
+  int4* items;      // [items] (sequence, its first and past-last row, the segment's first row),
+                    // longest first, then [items] ints: each one's number among the items
   int ptiles;       // 64-column tiles of d_v
   int step_items, step_parts;  // gridDim.x = step_items x (H x ptiles) + step_parts
 };
@@ -154,10 +155,35 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, S
     int b = 0;
     long long seg = 0;
     const bool ok = ssm_find_item(a.seq, item, sp.seg_rows, &b, &seg);
-    if (lane == 0)
-      items[item] = ok ? make_int4(b, (int)a.seq.start(b), (int)a.seq.end(b),
-                                   (int)(a.seq.start(b) + seg * sp.seg_rows))
-                       : make_int4(-1, 0, 0, 0);
+    // Longest first: CTAs that walk every gridDim.x-th piece then end at about the same time.  The
+    // place is the number of longer items and of equal ones before (bad offsets can make up
+    // more items than there are places: their order is left alone).
+    int place = item;
+    if (ok && a.seq.cu) {
+      const int whole = (int)(sp.seg_rows / SB_L);
+      auto blocks_of = [&](long long rows) { return (int)((rows + SB_L - 1) / SB_L); };
+      const long long own = a.seq.end(b) - a.seq.start(b) - seg * sp.seg_rows;
+      const int nb = blocks_of(own < sp.seg_rows ? own : sp.seg_rows);
+      int total = 0, before = 0;
+      for (int e = lane; e < a.seq.B; e += 32) {
+        const long long len = a.seq.end(e) - a.seq.start(e), full = len / sp.seg_rows;
+        const long long left = len - full * sp.seg_rows;
+        const int tail = left > 0 || len == 0, tail_nb = blocks_of(left);
+        total += (int)full + tail;
+        before += (whole > nb ? (int)full : 0) + (tail && tail_nb > nb);
+        if (e < b) before += (whole == nb ? (int)full : 0) + (tail && tail_nb == nb);
+        if (e == b && whole == nb) before += (int)(seg < full ? seg : full);
+      }
+      total = __reduce_add_sync(FULL_MASK, total);
+      before = __reduce_add_sync(FULL_MASK, before);
+      if (total <= n_items) place = before;
+    }
+    if (lane == 0) {
+      items[place] = ok ? make_int4(b, (int)a.seq.start(b), (int)a.seq.end(b),
+                                    (int)(a.seq.start(b) + seg * sp.seg_rows))
+                        : make_int4(-1, 0, 0, 0);
+      reinterpret_cast<int*>(items + n_items)[place] = item;
+    }
     return;
   }
   if (h >= a.H) return;
@@ -240,17 +266,17 @@ __device__ __forceinline__ void ssm_store_parts(uint8_t* place, uint32_t o0, uin
 // One piece of the scan's work: a segment of a sequence, a head and 64 of its columns.  A CTA
 // walks every gridDim.x-th piece.
 struct SsmPiece {
-  int item, part;  // work item, and its part: head + H x tile
-  int b, seq0, seq1, row0, row1, h, p0, nb;  // nb blocks
+  int place, part;  // place in the list of work items, and part: head + H x tile
+  int item, b, seq0, seq1, row0, row1, h, p0, nb;  // nb blocks
   __device__ __forceinline__ void begin(const SsmBlockArgs& ba) {
     const int parts = ba.a.H * ba.ptiles;
-    item = (int)blockIdx.x / parts;
-    part = (int)blockIdx.x - item * parts;
+    place = (int)blockIdx.x / parts;
+    part = (int)blockIdx.x - place * parts;
   }
   // The piece at hand; false past the last.
   __device__ __forceinline__ bool get(const SsmBlockArgs& ba) {
-    if (item >= ba.sp.items) return false;
-    const int4 at = __ldg(ba.items + item);
+    if (place >= ba.sp.items) return false;
+    const int4 at = __ldg(ba.items + place);
     const int H = ba.a.H;
     h = part;
     p0 = 0;
@@ -258,6 +284,7 @@ struct SsmPiece {
       h -= H;
       p0 += SB_P;
     }
+    item = __ldg(reinterpret_cast<const int*>(ba.items + ba.sp.items) + place);
     b = at.x;
     seq0 = at.y;
     seq1 = at.z;
@@ -268,12 +295,12 @@ struct SsmPiece {
     return b >= 0;
   }
   __device__ __forceinline__ void advance(const SsmBlockArgs& ba) {
-    item += ba.step_items;
+    place += ba.step_items;
     part += ba.step_parts;
     const int parts = ba.a.H * ba.ptiles;
     if (part >= parts) {
       part -= parts;
-      ++item;
+      ++place;
     }
   }
 };
