@@ -379,185 +379,188 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const int t = tid;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
-    for (int c = u0; c < u0 + w.nb; ++c) {
-      const uint32_t stage = c & 1;
-      ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_S + stage, c >> 1);
-      if (!ok) break;
-      tc_fence_after();
-      const SsmPrep& pr = *prep(c);
-      const uint32_t sbuf = tm + TM_S + stage * 128 + lanes;
-      const float in_t = pr.in[t];
-      float e = in_t;  // log2 decay from the end of run j up to t, j from warp - 1 down
-      float to[3];
+      for (int c = u0; c < u0 + w.nb; ++c) {
+        const uint32_t stage = c & 1;
+        ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_S + stage, c >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const SsmPrep& pr = *prep(c);
+        const uint32_t sbuf = tm + TM_S + stage * 128 + lanes;
+        const float in_t = pr.in[t];
+        float e = in_t;  // log2 decay from the end of run j up to t, j from warp - 1 down
+        float to[3];
 #pragma unroll
-      for (int j = 2; j >= 0; --j) {
-        to[j] = 0.0f;
-        if (j < warp) {
-          to[j] = fast_exp2(e);
-          e += pr.run[j];
+        for (int j = 2; j >= 0; --j) {
+          to[j] = 0.0f;
+          if (j < warp) {
+            to[j] = fast_exp2(e);
+            e += pr.run[j];
+          }
         }
-      }
-      // 16 columns at a time, the next 16 on their way from tensor memory; the row's warp needs
-      // the runs up to its own
-      const int groups = 2 * warp + 2;
-      float next[16];
-      tmem_ld16(sbuf, next);
+        // 16 columns at a time, the next 16 on their way from tensor memory; the row's warp needs
+        // the runs up to its own
+        const int groups = 2 * warp + 2;
+        float next[16];
+        tmem_ld16(sbuf, next);
 #pragma unroll 1
-      for (int grp = 0; grp < groups; ++grp) {
-        float s[16];
-        tmem_wait_ld();
+        for (int grp = 0; grp < groups; ++grp) {
+          float s[16];
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = next[i];
-        if (grp + 1 < groups) tmem_ld16(sbuf + 16 * (grp + 1), next);
-        uint32_t pk[8];
-        if (grp < 2 * warp) {
-          const float f = grp < 2 ? to[0] : grp < 4 ? to[1] : to[2];
-          const float2 f2 = make_float2(f, f);
-          const float4* o4 = reinterpret_cast<const float4*>(&pr.out[16 * grp]);
+          for (int i = 0; i < 16; ++i) s[i] = next[i];
+          if (grp + 1 < groups) tmem_ld16(sbuf + 16 * (grp + 1), next);
+          uint32_t pk[8];
+          if (grp < 2 * warp) {
+            const float f = grp < 2 ? to[0] : grp < 4 ? to[1] : to[2];
+            const float2 f2 = make_float2(f, f);
+            const float4* o4 = reinterpret_cast<const float4*>(&pr.out[16 * grp]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 o = o4[i];
-            const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
-                                  make_float2(s[4 * i], s[4 * i + 1]));
-            const float2 v = mul2(mul2(make_float2(o.z, o.w), f2),
-                                  make_float2(s[4 * i + 2], s[4 * i + 3]));
-            pk[2 * i] = pack_bf16(u.x, u.y);
-            pk[2 * i + 1] = pack_bf16(v.x, v.y);
+            for (int i = 0; i < 4; ++i) {
+              const float4 o = o4[i];
+              const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
+                                    make_float2(s[4 * i], s[4 * i + 1]));
+              const float2 v = mul2(mul2(make_float2(o.z, o.w), f2),
+                                    make_float2(s[4 * i + 2], s[4 * i + 3]));
+              pk[2 * i] = pack_bf16(u.x, u.y);
+              pk[2 * i + 1] = pack_bf16(v.x, v.y);
+            }
+          } else {
+            const float4* in4 = reinterpret_cast<const float4*>(&pr.in[16 * grp]);
+            const float4* d4 = reinterpret_cast<const float4*>(&pr.d[16 * grp]);
+            const float2 t2 = make_float2(in_t, in_t);
+            const int own = t - 16 * grp;  // the row's own column among these
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 in = in4[i], d = d4[i];
+              const float2 e0 = sub2(t2, make_float2(in.x, in.y)),
+                           e1 = sub2(t2, make_float2(in.z, in.w));
+              float2 u = mul2(mul2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(d.x, d.y)),
+                              make_float2(fast_exp2(e0.x), fast_exp2(e0.y)));
+              float2 v = mul2(mul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(d.z, d.w)),
+                              make_float2(fast_exp2(e1.x), fast_exp2(e1.y)));
+              if (4 * i > own) u.x = 0.0f;
+              if (4 * i + 1 > own) u.y = 0.0f;
+              if (4 * i + 2 > own) v.x = 0.0f;
+              if (4 * i + 3 > own) v.y = 0.0f;
+              pk[2 * i] = pack_bf16(u.x, u.y);
+              pk[2 * i + 1] = pack_bf16(v.x, v.y);
+            }
           }
-        } else {
-          const float4* in4 = reinterpret_cast<const float4*>(&pr.in[16 * grp]);
-          const float4* d4 = reinterpret_cast<const float4*>(&pr.d[16 * grp]);
-          const float2 t2 = make_float2(in_t, in_t);
-          const int own = t - 16 * grp;  // the row's own column among these
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 in = in4[i], d = d4[i];
-            const float2 e0 = sub2(t2, make_float2(in.x, in.y)),
-                         e1 = sub2(t2, make_float2(in.z, in.w));
-            float2 u = mul2(mul2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(d.x, d.y)),
-                            make_float2(fast_exp2(e0.x), fast_exp2(e0.y)));
-            float2 v = mul2(mul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(d.z, d.w)),
-                            make_float2(fast_exp2(e1.x), fast_exp2(e1.y)));
-            if (4 * i > own) u.x = 0.0f;
-            if (4 * i + 1 > own) u.y = 0.0f;
-            if (4 * i + 2 > own) v.x = 0.0f;
-            if (4 * i + 3 > own) v.y = 0.0f;
-            pk[2 * i] = pack_bf16(u.x, u.y);
-            pk[2 * i + 1] = pack_bf16(v.x, v.y);
-          }
+          // P's columns 8 grp .. lie in columns of S that are already read
+          tmem_st8(sbuf + 8 * grp, pk);
         }
-        // P's columns 8 grp .. lie in columns of S that are already read
-        tmem_st8(sbuf + 8 * grp, pk);
+        {
+          const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          for (int grp = groups; grp < 8; ++grp) tmem_st8(sbuf + 8 * grp, none);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(BAR_P + stage));
+          mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
+        }
       }
-      {
-        const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int grp = groups; grp < 8; ++grp) tmem_st8(sbuf + 8 * grp, none);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(BAR_P + stage));
-        mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
-      }
-    }
   } else if (warp < 8) {
     // ------------------------------------------------ Y: row t = tid - 128
     const int t = tid - 128, quad = warp - 4;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     for (; ok && w.get(ba); u0 += w.nb, w.advance(ba)) {
-    const float D = a.D ? a.D[w.h] : 0.0f;
-    const float2 D2 = make_float2(D, D);
-    const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;  // columns that exist
-    __nv_bfloat16* const yp = static_cast<__nv_bfloat16*>(a.y) + (size_t)w.h * a.P + w.p0;
-    const __nv_bfloat16* const zp =
-        a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)w.h * a.P + w.p0 : nullptr;
-    // whole sectors where rows start on them and hold a multiple of 16 values
-    const bool sectors = a.P % 16 == 0 && a.gate_stride % 16 == 0 &&
-                         ((reinterpret_cast<uintptr_t>(yp) | reinterpret_cast<uintptr_t>(zp)) & 31) == 0;
-    for (int c = u0; c < u0 + w.nb; ++c) {
-      const uint32_t stage = c & 1;
-      const int row = w.row0 + (c - u0) * SB_L + t;
-      const bool live = row < w.row1;
-      const __nv_bfloat16* const zrow = zp + (long long)row * a.gate_stride;
-      __nv_bfloat16* const yrow = yp + (size_t)row * a.H * a.P;
-      ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
-      if (!ok) break;
-      float decay;  // from the block's start up to t
-      {
-        const SsmPrep& pr = *prep(c);
-        float e = pr.in[t];
+      const float D = a.D ? a.D[w.h] : 0.0f;
+      const float2 D2 = make_float2(D, D);
+      const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;  // columns that exist
+      __nv_bfloat16* const yp = static_cast<__nv_bfloat16*>(a.y) + (size_t)w.h * a.P + w.p0;
+      const __nv_bfloat16* const zp =
+          a.gate ? static_cast<const __nv_bfloat16*>(a.gate) + (size_t)w.h * a.P + w.p0 : nullptr;
+      // whole sectors where rows start on them and hold a multiple of 16 values
+      const uintptr_t bases = reinterpret_cast<uintptr_t>(yp) | reinterpret_cast<uintptr_t>(zp);
+      const bool sectors = a.P % 16 == 0 && a.gate_stride % 16 == 0 && (bases & 31) == 0;
+      for (int c = u0; c < u0 + w.nb; ++c) {
+        const uint32_t stage = c & 1;
+        const int row = w.row0 + (c - u0) * SB_L + t;
+        const bool live = row < w.row1;
+        const __nv_bfloat16* const zrow = zp + (long long)row * a.gate_stride;
+        __nv_bfloat16* const yrow = yp + (size_t)row * a.H * a.P;
+        ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
+        if (!ok) break;
+        float decay;  // from the block's start up to t
+        {
+          const SsmPrep& pr = *prep(c);
+          float e = pr.in[t];
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-          if (j < quad) e += pr.run[j];
-        decay = fast_exp2(e);
-      }
-      const float2 f2 = make_float2(decay, decay);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
-      uint32_t z[8];
-      auto load_z = [&](int part) {
-        if (!zp || !live || 16 * part >= pn) return;
-        if (sectors) {
-          load_sector(zrow + 16 * part, z);
-        } else {
-          *reinterpret_cast<uint4*>(z) = *reinterpret_cast<const uint4*>(zrow + 16 * part);
-          if (16 * part + 8 < pn)
-            *reinterpret_cast<uint4*>(z + 4) = *reinterpret_cast<const uint4*>(zrow + 16 * part + 8);
+          for (int j = 0; j < 3; ++j)
+            if (j < quad) e += pr.run[j];
+          decay = fast_exp2(e);
         }
-      };
-      load_z(0);  // on its way while the products finish
-      ok = wait(BAR_Y2 + stage, c >> 1) && wait(BAR_Y + stage, c >> 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
-      const uint32_t ybuf = tm + TM_S + stage * 128 + TM_Y1 + lanes, y2buf = tm + TM_Y2 + stage * 64 + lanes;
-#pragma unroll 1
-      for (int part = 0; part < 4; ++part) {
-        float y1[16], y2[16];
-        tmem_ld16(ybuf + 16 * part, y1);
-        tmem_ld16(y2buf + 16 * part, y2);
-        const uint4 va = *reinterpret_cast<const uint4*>(vtile + tile_offset(t, 2 * part)),
-                    vb = *reinterpret_cast<const uint4*>(vtile + tile_offset(t, 2 * part + 1));
-        const uint32_t vw[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-        float2 o[8];
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[j] = fma2(D2, unpack_bf16(vw[j]),
-                      fma2(f2, make_float2(y2[2 * j], y2[2 * j + 1]),
-                           make_float2(y1[2 * j], y1[2 * j + 1])));
-        }
-        if (zp) {
-          float2 g[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = unpack_bf16(z[j]);
-          fast_act<8>(g, a.act);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = mul2(o[j], g[j]);
-          if (part < 3) load_z(part + 1);
-        }
-        uint32_t out[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) out[j] = pack_bf16(o[j].x, o[j].y);
-        if (live && 16 * part < pn) {
+        const float2 f2 = make_float2(decay, decay);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
+        uint32_t z[8];
+        auto load_z = [&](int part) {
+          if (!zp || !live || 16 * part >= pn) return;
           if (sectors) {
-            store_sector(yrow + 16 * part, out);
+            load_sector(zrow + 16 * part, z);
           } else {
-            *reinterpret_cast<uint4*>(yrow + 16 * part) = make_uint4(out[0], out[1], out[2], out[3]);
+            *reinterpret_cast<uint4*>(z) = *reinterpret_cast<const uint4*>(zrow + 16 * part);
             if (16 * part + 8 < pn)
-              *reinterpret_cast<uint4*>(yrow + 16 * part + 8) =
-                  make_uint4(out[4], out[5], out[6], out[7]);
+              *reinterpret_cast<uint4*>(z + 4) =
+                  *reinterpret_cast<const uint4*>(zrow + 16 * part + 8);
+          }
+        };
+        load_z(0);  // on its way while the products finish
+        ok = wait(BAR_Y2 + stage, c >> 1) && wait(BAR_Y + stage, c >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
+        const uint32_t ybuf = tm + TM_S + stage * 128 + TM_Y1 + lanes,
+                       y2buf = tm + TM_Y2 + stage * 64 + lanes;
+#pragma unroll 1
+        for (int part = 0; part < 4; ++part) {
+          float y1[16], y2[16];
+          tmem_ld16(ybuf + 16 * part, y1);
+          tmem_ld16(y2buf + 16 * part, y2);
+          const uint4 va = *reinterpret_cast<const uint4*>(vtile + tile_offset(t, 2 * part)),
+                      vb = *reinterpret_cast<const uint4*>(vtile + tile_offset(t, 2 * part + 1));
+          const uint32_t vw[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+          float2 o[8];
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            o[j] = fma2(D2, unpack_bf16(vw[j]),
+                        fma2(f2, make_float2(y2[2 * j], y2[2 * j + 1]),
+                             make_float2(y1[2 * j], y1[2 * j + 1])));
+          }
+          if (zp) {
+            float2 g[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = unpack_bf16(z[j]);
+            fast_act<8>(g, a.act);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = mul2(o[j], g[j]);
+            if (part < 3) load_z(part + 1);
+          }
+          uint32_t out[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) out[j] = pack_bf16(o[j].x, o[j].y);
+          if (live && 16 * part < pn) {
+            if (sectors) {
+              store_sector(yrow + 16 * part, out);
+            } else {
+              *reinterpret_cast<uint4*>(yrow + 16 * part) =
+                  make_uint4(out[0], out[1], out[2], out[3]);
+              if (16 * part + 8 < pn)
+                *reinterpret_cast<uint4*>(yrow + 16 * part + 8) =
+                    make_uint4(out[4], out[5], out[6], out[7]);
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(BAR_YFREE + stage));
+          mbar_arrive(bar(BAR_VFREE + (c & 3)));
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(BAR_YFREE + stage));
-        mbar_arrive(bar(BAR_VFREE + (c & 3)));
-      }
-    }
     }
   } else if (warp < 12) {
     // ------------------------------------------------ H: row n = tid - 256
@@ -585,165 +588,164 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       if (lane == 0) mbar_arrive(bar(BAR_HREADY));
     };
     for (; ok && w.get(ba); u0 += w.nb, w.advance(ba)) {
-    const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
-    float* const mrow = a.M + (((size_t)w.b * a.H + w.h) * a.N + n) * a.P + w.p0;
-    const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
-    const float* const from =
-        split ? ba.sp.starts + (((size_t)w.item * a.H + w.h) * a.N + n) * a.P + w.p0 : mrow;
+      const int pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
+      float* const mrow = a.M + (((size_t)w.b * a.H + w.h) * a.N + n) * a.P + w.p0;
+      const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
+      const float* const from =
+          split ? ba.sp.starts + (((size_t)w.item * a.H + w.h) * a.N + n) * a.P + w.p0 : mrow;
 #pragma unroll
-    for (int i = 0; i < SB_P; i += 4) {
-      float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-      if ((split || !a.from_zero) && n < a.N && i < pn)
-        m = *reinterpret_cast<const float4*>(from + i);
-      st[i / 2] = make_float2(m.x, m.y);
-      st[i / 2 + 1] = make_float2(m.z, m.w);
-    }
-    if (w.nb > 0) {  // the state before the piece; the last block before has read its own
-      ok = u0 == 0 || wait(BAR_HFREE, u0 - 1);
-      if (!ok) break;
-#pragma unroll
-      for (int ch = 0; ch < 8; ++ch) publish(ch);
-      published();
-    }
-    for (int c = u0; c < u0 + w.nb; ++c) {
-      ok = wait(BAR_PREP + (c & 3), c >> 2);
-      if (!ok) break;
-      const SsmPrep& pr = *prep(c);
-      const float keep = exp2f((pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
-      ok = wait(BAR_DM + (c & 1), c >> 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t dm = tm + TM_DM + (c & 1) * 64 + lanes;
-#pragma unroll
-      for (int part = 0; part < 4; ++part) {
-        float r[16];
-        tmem_ld16(dm + 16 * part, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          // one by one: as pairs the state would be held twice, and spilled
-          st[8 * part + i] = make_float2(fmaf(st[8 * part + i].x, keep, r[2 * i]),
-                                         fmaf(st[8 * part + i].y, keep, r[2 * i + 1]));
+      for (int i = 0; i < SB_P; i += 4) {
+        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+        if ((split || !a.from_zero) && n < a.N && i < pn)
+          m = *reinterpret_cast<const float4*>(from + i);
+        st[i / 2] = make_float2(m.x, m.y);
+        st[i / 2 + 1] = make_float2(m.z, m.w);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_DMFREE + (c & 1)));
-      if (c + 1 < u0 + w.nb) {
-        ok = wait(BAR_HFREE, c);
+      if (w.nb > 0) {  // the state before the piece; the last block before has read its own
+        ok = u0 == 0 || wait(BAR_HFREE, u0 - 1);
         if (!ok) break;
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) publish(ch);
         published();
       }
-    }
-    if (ok && w.row1 == w.seq1 && n < a.N) {
+      for (int c = u0; c < u0 + w.nb; ++c) {
+        ok = wait(BAR_PREP + (c & 3), c >> 2);
+        if (!ok) break;
+        const SsmPrep& pr = *prep(c);
+        const float keep = exp2f((pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
+        ok = wait(BAR_DM + (c & 1), c >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dm = tm + TM_DM + (c & 1) * 64 + lanes;
 #pragma unroll
-      for (int i = 0; i < SB_P; i += 4)
-        if (i < pn)
-          *reinterpret_cast<float4*>(mrow + i) =
-              make_float4(st[i / 2].x, st[i / 2].y, st[i / 2 + 1].x, st[i / 2 + 1].y);
-    }
+        for (int part = 0; part < 4; ++part) {
+          float r[16];
+          tmem_ld16(dm + 16 * part, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            // one by one: as pairs the state would be held twice, and spilled
+            st[8 * part + i] = make_float2(fmaf(st[8 * part + i].x, keep, r[2 * i]),
+                                           fmaf(st[8 * part + i].y, keep, r[2 * i + 1]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_DMFREE + (c & 1)));
+        if (c + 1 < u0 + w.nb) {
+          ok = wait(BAR_HFREE, c);
+          if (!ok) break;
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) publish(ch);
+          published();
+        }
+      }
+      if (ok && w.row1 == w.seq1 && n < a.N) {
+#pragma unroll
+        for (int i = 0; i < SB_P; i += 4)
+          if (i < pn)
+            *reinterpret_cast<float4*>(mrow + i) =
+                make_float4(st[i / 2].x, st[i / 2].y, st[i / 2 + 1].x, st[i / 2 + 1].y);
+      }
     }
   } else if (warp < 16) {
     // ------------------------------------------------ W: three bf16 parts of w o v
     const int i0 = tid - 384, rq = i0 >> 2;  // row in the quarter, and 16 of its values
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
     for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
-    for (int c = u0; c < u0 + w.nb; ++c) {
-      const int stage = c & 1;
-      ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
-      if (!ok) break;
-      uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
-      const float* weights = prep(c)->w;
-      const int left = w.row1 - (w.row0 + (c - u0) * SB_L);
-      if (left < SB_L) {
-        // rows behind the segment's end, whatever they hold, become zeros
-        ok = wait(BAR_KFULL + stage, c >> 1);
+      for (int c = u0; c < u0 + w.nb; ++c) {
+        const int stage = c & 1;
+        ok = wait(BAR_PREP + (c & 3), c >> 2) && wait(BAR_VFULL + (c & 3), c >> 2);
         if (!ok) break;
-        for (int t = rq; t < SB_L; t += 32) {
-          if (t < left) continue;
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t o = (i ? o1 : o0) + (t - rq) * 128;
-            *reinterpret_cast<uint4*>(vtile + o) = make_uint4(0, 0, 0, 0);
-            for (int pl = 0; pl < npanels; ++pl)
-              *reinterpret_cast<uint4*>(sm + SB_K + (2 * stage + pl) * SB_PANEL + o) =
-                  make_uint4(0, 0, 0, 0);
+        uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
+        const float* weights = prep(c)->w;
+        const int left = w.row1 - (w.row0 + (c - u0) * SB_L);
+        if (left < SB_L) {
+          // rows behind the segment's end, whatever they hold, become zeros
+          ok = wait(BAR_KFULL + stage, c >> 1);
+          if (!ok) break;
+          for (int t = rq; t < SB_L; t += 32) {
+            if (t < left) continue;
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t o = (i ? o1 : o0) + (t - rq) * 128;
+              *reinterpret_cast<uint4*>(vtile + o) = make_uint4(0, 0, 0, 0);
+              for (int pl = 0; pl < npanels; ++pl)
+                *reinterpret_cast<uint4*>(sm + SB_K + (2 * stage + pl) * SB_PANEL + o) =
+                    make_uint4(0, 0, 0, 0);
+            }
           }
         }
-      }
-      uint4 na = *reinterpret_cast<const uint4*>(vtile + o0),
-            nb4 = *reinterpret_cast<const uint4*>(vtile + o1);
-      float nw = weights[rq];
+        uint4 na = *reinterpret_cast<const uint4*>(vtile + o0),
+              nb4 = *reinterpret_cast<const uint4*>(vtile + o1);
+        float nw = weights[rq];
 #pragma unroll 1
-      for (int qd = 0; qd < 4; ++qd) {
-        const int use = 4 * c + qd, buf = qd & 1;
-        uint32_t p[3][8];
-        ssm_parts(na, nb4, nw, p);
-        if (qd < 3) {
-          na = *reinterpret_cast<const uint4*>(vtile + 4096 * (qd + 1) + o0);
-          nb4 = *reinterpret_cast<const uint4*>(vtile + 4096 * (qd + 1) + o1);
-          nw = weights[32 * (qd + 1) + rq];
+        for (int qd = 0; qd < 4; ++qd) {
+          const int use = 4 * c + qd, buf = qd & 1;
+          uint32_t p[3][8];
+          ssm_parts(na, nb4, nw, p);
+          if (qd < 3) {
+            na = *reinterpret_cast<const uint4*>(vtile + 4096 * (qd + 1) + o0);
+            nb4 = *reinterpret_cast<const uint4*>(vtile + 4096 * (qd + 1) + o1);
+            nw = weights[32 * (qd + 1) + rq];
+          }
+          ok = use < 2 || wait(BAR_WFREE + buf, (use >> 1) - 1);
+          if (!ok) break;
+          ssm_store_parts(sm + SB_W + buf * 3 * SB_WPART, o0, o1, p);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(BAR_WREADY + buf));
         }
-        ok = use < 2 || wait(BAR_WFREE + buf, (use >> 1) - 1);
         if (!ok) break;
-        ssm_store_parts(sm + SB_W + buf * 3 * SB_WPART, o0, o1, p);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_WREADY + buf));
+        if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
       }
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
-    }
-  } else if (warp >= 16) {
-  if (warp == 18) {
+  } else if (warp == 18) {
     // ------------------------------------------------ products Y2 of a block and S of the next
     constexpr uint32_t dS = mma_desc(128, 128, 0, 0), dY2 = mma_desc(128, 64, 0, 1);
     const uint32_t q0 = tile_desc(base + SB_Q), k0 = tile_desc(base + SB_K),
                    h0 = tile_desc(base + SB_H);
     for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
-    for (int c = u0 - 1; c < u0 + w.nb; ++c) {
-      if (c >= u0) {
-        const uint32_t stage = c & 1;
-        // the block's buffer of Y2 is free since its S was issued: group Y reads both
-        ok = wait(BAR_HREADY, c);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
+      for (int c = u0 - 1; c < u0 + w.nb; ++c) {
+        if (c >= u0) {
+          const uint32_t stage = c & 1;
+          // the block's buffer of Y2 is free since its S was issued: group Y reads both
+          ok = wait(BAR_HREADY, c);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t o = ((i >> 2 & 1) * SB_PANEL + (i & 3) * 32) >> 4;
-            if ((i & 7) < nk)
-              mma_ss(tm + TM_Y2 + stage * 64, q0 + o,
-                     h0 + (((i >> 3) * SB_PANEL + (i & 7) * 2048) >> 4), dY2, i > 0);
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t o = ((i >> 2 & 1) * SB_PANEL + (i & 3) * 32) >> 4;
+              if ((i & 7) < nk)
+                mma_ss(tm + TM_Y2 + stage * 64, q0 + o,
+                       h0 + (((i >> 3) * SB_PANEL + (i & 7) * 2048) >> 4), dY2, i > 0);
+            }
+            mma_commit(bar(BAR_Y2 + stage));
+            mma_commit(bar(BAR_HFREE));
+            mma_commit(bar(BAR_QFREE));
           }
-          mma_commit(bar(BAR_Y2 + stage));
-          mma_commit(bar(BAR_HFREE));
-          mma_commit(bar(BAR_QFREE));
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      const int e = c + 1;
-      if (e < u0 + w.nb) {
-        const uint32_t stage = e & 1;
-        ok = wait(BAR_QFULL, e) && wait(BAR_KFULL + stage, e >> 1) &&
-             (e < 2 || wait(BAR_YFREE + stage, (e >> 1) - 1));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t k = k0 + stage * (2 * SB_PANEL >> 4);
+        const int e = c + 1;
+        if (e < u0 + w.nb) {
+          const uint32_t stage = e & 1;
+          ok = wait(BAR_QFULL, e) && wait(BAR_KFULL + stage, e >> 1) &&
+               (e < 2 || wait(BAR_YFREE + stage, (e >> 1) - 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t k = k0 + stage * (2 * SB_PANEL >> 4);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t o = ((i >> 2) * SB_PANEL + (i & 3) * 32) >> 4;
-            if (i < nk) mma_ss(tm + TM_S + stage * 128, q0 + o, k + o, dS, i > 0);
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t o = ((i >> 2) * SB_PANEL + (i & 3) * 32) >> 4;
+              if (i < nk) mma_ss(tm + TM_S + stage * 128, q0 + o, k + o, dS, i > 0);
+            }
+            mma_commit(bar(BAR_S + stage));
+            mma_commit(bar(BAR_KFREE + stage));
           }
-          mma_commit(bar(BAR_S + stage));
-          mma_commit(bar(BAR_KFREE + stage));
+          __syncwarp();
         }
-        __syncwarp();
       }
-    }
     if (elect_one()) mma_commit(bar(BAR_DRAIN));
     __syncwarp();
     ok = mbar_wait(bar(BAR_DRAIN), 0) && ok;
@@ -753,43 +755,43 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     const uint32_t k0 = tile_desc(base + SB_K, SB_PANEL), w0 = tile_desc(base + SB_W),
                    v0 = tile_desc(base + SB_V);
     for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
-    for (int c = u0; c < u0 + w.nb && ok; ++c) {
-      const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
-      ok = wait(BAR_KFULL + stage, c >> 1) &&
-           (c < 2 || wait(BAR_DMFREE + stage, (c >> 1) - 1));
-      for (int qd = 0; qd < 4 && ok; ++qd) {
-        const uint32_t use = 4 * c + qd, buf = use & 1;
-        ok = wait(BAR_WREADY + buf, use >> 1);
+      for (int c = u0; c < u0 + w.nb && ok; ++c) {
+        const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
+        ok = wait(BAR_KFULL + stage, c >> 1) &&
+             (c < 2 || wait(BAR_DMFREE + stage, (c >> 1) - 1));
+        for (int qd = 0; qd < 4 && ok; ++qd) {
+          const uint32_t use = 4 * c + qd, buf = use & 1;
+          ok = wait(BAR_WREADY + buf, use >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t kq = k + qd * (4096 >> 4), wb = w0 + buf * (3 * SB_WPART >> 4);
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+              mma_ss(tm + TM_DM + stage * 64, kq + (i & 1) * (2048 >> 4),
+                     wb + (((i >> 1) * SB_WPART + (i & 1) * 2048) >> 4), dM, qd + i > 0);
+            mma_commit(bar(BAR_WFREE + buf));
+            if (qd == 3) {
+              mma_commit(bar(BAR_DM + stage));
+              mma_commit(bar(BAR_KFREE + stage));
+            }
+          }
+          __syncwarp();
+        }
+        // the last quarter is also the sign that v's rows behind the end are zeros
+        ok = ok && wait(BAR_VFULL + (c & 3), c >> 2) && wait(BAR_P + stage, c >> 1);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t slot = c & 3;
         if (elect_one()) {
-          const uint32_t kq = k + qd * (4096 >> 4), wb = w0 + buf * (3 * SB_WPART >> 4);
+          const uint32_t v = v0 + slot * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
 #pragma unroll
-          for (int i = 0; i < 6; ++i)
-            mma_ss(tm + TM_DM + stage * 64, kq + (i & 1) * (2048 >> 4),
-                   wb + (((i >> 1) * SB_WPART + (i & 1) * 2048) >> 4), dM, qd + i > 0);
-          mma_commit(bar(BAR_WFREE + buf));
-          if (qd == 3) {
-            mma_commit(bar(BAR_DM + stage));
-            mma_commit(bar(BAR_KFREE + stage));
-          }
+          for (int i = 0; i < SB_L / 16; ++i)
+            mma_ts(s + TM_Y1, s + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
+          mma_commit(bar(BAR_Y + stage));
         }
         __syncwarp();
       }
-      // the last quarter is also the sign that v's rows behind the end are zeros
-      ok = ok && wait(BAR_VFULL + (c & 3), c >> 2) && wait(BAR_P + stage, c >> 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t slot = c & 3;
-      if (elect_one()) {
-        const uint32_t v = v0 + slot * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
-#pragma unroll
-        for (int i = 0; i < SB_L / 16; ++i)
-          mma_ts(s + TM_Y1, s + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
-        mma_commit(bar(BAR_Y + stage));
-      }
-      __syncwarp();
-    }
     if (elect_one()) mma_commit(bar(BAR_DRAIN + 1));
     __syncwarp();
     ok = mbar_wait(bar(BAR_DRAIN + 1), 0) && ok;
@@ -868,7 +870,6 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       for (int c = vc > 4 ? vc - 4 : 0; c < vc; ++c)
         mbar_wait(bar(BAR_VFULL + (c & 3)), (uint32_t)(c >> 2) & 1u);
     }
-  }
   }
   tc_fence_before();
   __syncthreads();
@@ -961,59 +962,59 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
     const uint32_t o0 = tile_offset(rq, 2 * (i0 & 3)), o1 = tile_offset(rq, 2 * (i0 & 3) + 1);
     int stage = 0, round = 0;
     while (next_piece()) {
-    const int u0 = turn * nb;
-    float carry = 0.0f;  // log2 decay of the blocks behind
-    for (int c = 0; c < nb && ok; ++c) {
-      ok = wait(GB_FULL + stage, round);
-      if (!ok) break;
-      const uint8_t* vtile = sm + SG_V + stage * SB_PANEL;
-      const SsmPrep& pr = *prep(stage);
-      const float f = exp2f(carry);
-      carry += (pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]);
+      const int u0 = turn * nb;
+      float carry = 0.0f;  // log2 decay of the blocks behind
+      for (int c = 0; c < nb && ok; ++c) {
+        ok = wait(GB_FULL + stage, round);
+        if (!ok) break;
+        const uint8_t* vtile = sm + SG_V + stage * SB_PANEL;
+        const SsmPrep& pr = *prep(stage);
+        const float f = exp2f(carry);
+        carry += (pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int qd = 2 * i + grp;  // the group's buffers: qd
-        uint32_t p[3][8];
-        ssm_parts(*reinterpret_cast<const uint4*>(vtile + 4096 * qd + o0),
-                  *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o1),
-                  pr.w[32 * qd + rq] * f, p);
-        ok = ok && (u0 + c == 0 || wait(GB_WFREE + qd, u0 + c - 1));
-        ssm_store_parts(sm + SG_W + qd * 3 * SB_WPART, o0, o1, p);
-        fence_async_smem();
+        for (int i = 0; i < 2; ++i) {
+          const int qd = 2 * i + grp;  // the group's buffers: qd
+          uint32_t p[3][8];
+          ssm_parts(*reinterpret_cast<const uint4*>(vtile + 4096 * qd + o0),
+                    *reinterpret_cast<const uint4*>(vtile + 4096 * qd + o1),
+                    pr.w[32 * qd + rq] * f, p);
+          ok = ok && (u0 + c == 0 || wait(GB_WFREE + qd, u0 + c - 1));
+          ssm_store_parts(sm + SG_W + qd * 3 * SB_WPART, o0, o1, p);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(GB_WREADY + qd));
+        }
+        if (++stage == SG_STAGES) {
+          stage = 0;
+          ++round;
+        }
+      }
+      if (tid == 0 && w.p0 == 0) ba.sp.decays[(size_t)w.item * a.H + w.h] = exp2f(carry);
+      if (warp < 4 && ok) {
+        ok = wait(GB_DONE, turn);
+        if (!ok) break;
+        tc_fence_after();
+        const int n = tid, pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        // the state before the next segment gets this one's contribution
+        float* to = ba.sp.starts + (((size_t)(w.item + 1) * a.H + w.h) * a.N + n) * a.P + w.p0;
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          float r1[16], r2[16];
+          tmem_ld16(tm + 16 * part + lanes, r1);
+          tmem_ld16(tm + 64 + 16 * part + lanes, r2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            if (n < a.N && 16 * part + i < pn)
+              *reinterpret_cast<float4*>(to + 16 * part + i) =
+                  make_float4(r1[i] + r2[i], r1[i + 1] + r2[i + 1], r1[i + 2] + r2[i + 2],
+                              r1[i + 3] + r2[i + 3]);
+        }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(GB_WREADY + qd));
+        if (lane == 0) mbar_arrive(bar(GB_READ));
       }
-      if (++stage == SG_STAGES) {
-        stage = 0;
-        ++round;
-      }
-    }
-    if (tid == 0 && w.p0 == 0) ba.sp.decays[(size_t)w.item * a.H + w.h] = exp2f(carry);
-    if (warp < 4 && ok) {
-      ok = wait(GB_DONE, turn);
-      if (!ok) break;
-      tc_fence_after();
-      const int n = tid, pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
-      const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-      // the state before the next segment gets this one's contribution
-      float* to = ba.sp.starts + (((size_t)(w.item + 1) * a.H + w.h) * a.N + n) * a.P + w.p0;
-#pragma unroll
-      for (int part = 0; part < 4; ++part) {
-        float r1[16], r2[16];
-        tmem_ld16(tm + 16 * part + lanes, r1);
-        tmem_ld16(tm + 64 + 16 * part + lanes, r2);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          if (n < a.N && 16 * part + i < pn)
-            *reinterpret_cast<float4*>(to + 16 * part + i) =
-                make_float4(r1[i] + r2[i], r1[i + 1] + r2[i + 1], r1[i + 2] + r2[i + 2],
-                            r1[i + 3] + r2[i + 3]);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(GB_READ));
-    }
     }
   } else if (warp == 8) {
     constexpr uint32_t dM = mma_desc(128, 128, 1, 1), dM2 = mma_desc(128, 64, 1, 1);

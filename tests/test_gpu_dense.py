@@ -324,6 +324,28 @@ def test_ssm_step_sizes(sdm, softplus, act):
     ref.check(M, rM, Mb, "M")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("low", [float("-inf"), "lowest"])
+def test_ssm_padding_by_the_step_size(sdm, dt, low):
+    """Tokens whose dt is -infinity or the type's lowest value leave the state as it is: left and
+    right padding of a batch gives the states of the sequences without it."""
+    t, H, N, P = TYPES[dt], 2, 64, 64
+    low = torch.finfo(t).min if low == "lowest" else low
+    i, M = ssm_inputs(gen(41), (1, 400), H, 1, N, P, t, False, True, 1)
+    own = {k: (x[:, 37:300].contiguous() if k in ("k", "q", "v", "dt") and x is not None else x)
+           for k, x in i.items()}
+    Mo = M.clone()
+    yo = sdm.sdm_ssm_forward(M=Mo, init="continue", **own)
+    i["dt"][:, :37] = low
+    i["dt"][:, 300:] = low
+    y = sdm.sdm_ssm_forward(M=M, init="continue", **i)
+    # the same terms in other blocks: fp32 rounding of the state, one bf16 weight and y's own
+    assert (M - Mo).norm() <= 2e-6 * Mo.norm()
+    tol = 4 * 2.0 ** -8 if dt == "bf16" else 2e-6
+    assert (y[:, 37:300].float() - yo.float()).norm() <= tol * yo.float().norm()
+    assert torch.isfinite(y).all()
+
+
 def test_ssm_neighbours_do_not_mix(sdm):
     """A sequence of NaN and infinity next to others changes no bit of theirs."""
     lens = [200, 133, 270]
