@@ -394,9 +394,9 @@ size_t sdm_ssm_workspace_size(sdm_ssm_shape shape);
  *   it is left as it is after the last token; y [B,T,H,d_v] in_dtype, contiguous.
  * ws / ws_bytes: at least sdm_ssm_workspace_size bytes, 256-byte aligned, NULL if that is 0;
  * calls that overlap on the GPU need one each.
- * k, q and v have to be finite: a NaN or infinity also reaches other tokens of its sequence
- * (never another sequence).  dt of -infinity, or a type's lowest value, is a step of size 0: the
- * token (padding, for instance) leaves the state as it is.
+ * k, q, v and dt have to be finite: a NaN or infinity also reaches other tokens of its sequence
+ * (never another sequence).  Only dt may be -infinity: it, or a type's lowest value, is a step of
+ * size 0, and the token (padding, for instance) leaves the state as it is.
  */
 sdm_status sdm_ssm_forward(const void *k, const void *q, const void *v, const void *dt,
                            const float *A, const float *dt_bias, const float *D, float *M,

@@ -201,8 +201,8 @@ def test_ssm_packed(sdm, dt, lens, init):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T,H,N,P,init", [
-    (1, 5000, 2, 128, 64, "continue"), (2, 2437, 3, 64, 128, "zero"), (1, 4096, 1, 16, 40, "continue"),
-    (1, 1500, 1, 200, 24, "continue"),
+    (1, 5000, 2, 128, 64, "continue"), (2, 2437, 3, 64, 128, "zero"),
+    (1, 4096, 1, 16, 40, "continue"), (1, 1500, 1, 200, 24, "continue"),
 ])
 def test_ssm_long(sdm, dt, B, T, H, N, P, init):
     """Prompts that are cut into segments (few heads, many blocks)."""
@@ -322,6 +322,55 @@ def test_ssm_step_sizes(sdm, softplus, act):
     ry, rM, yb, Mb = ssm_ref(i, M0, [T], "bf16", softplus, act)
     ref.check(y.reshape(T, H, P), ry, yb, "y")
     ref.check(M, rM, Mb, "M")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_far_apart(sdm, dt):
+    """Pitched rows that reach past 2^31 elements: the same bits as contiguous rows."""
+    t, H, N, P, T, pitch = TYPES[dt], 2, 32, 24, 40, 1 << 26
+    i, M = ssm_inputs(gen(42), (1, T), H, 1, N, P, t, False, True, 1)
+    far = torch.empty((T, pitch), dtype=t, device="cuda")
+    views, at = {}, 0
+    for name in ("k", "q", "v", "dt"):
+        x = i[name]
+        width = x[0, 0].numel()
+        far[:, at:at + width] = x.reshape(T, width)
+        views[name] = far[:, at:at + width].view((1, T) + x.shape[2:])
+        at += (width + 7) // 8 * 8
+    M1, M2 = M.clone(), M.clone()
+    y1 = sdm.sdm_ssm_forward(M=M1, init="continue", **i)
+    y2 = sdm.sdm_ssm_forward(M=M2, init="continue", **{**i, **views})
+    assert torch.equal(y1, y2) and torch.equal(M1, M2)
+    one = {n: x[0] for n, x in i.items() if n in views}
+    rest = {n: x for n, x in i.items() if n not in views}
+    B = T  # the same rows as one token of each of T sequences
+    M1 = M.expand(B, -1, -1, -1).contiguous()
+    M2 = M1.clone()
+    y1 = sdm.sdm_ssm_step(M=M1, **one, **rest)
+    y2 = sdm.sdm_ssm_step(M=M2, **{n: x[0] for n, x in views.items()}, **rest)
+    assert torch.equal(y1, y2) and torch.equal(M1, M2)
+    w = torch.randn(P * H, 4, device="cuda")
+    x, xf = i["v"].reshape(1, T, -1), views["v"].view(1, T, -1)
+    assert torch.equal(sdm.sdm_conv_forward(x, w), sdm.sdm_conv_forward(xf, w))
+
+
+def test_ssm_large_state(sdm):
+    """A batch whose state has more than 2^31 values: its last sequences are as on their own."""
+    B, N, P = 33000, 256, 256
+    M = torch.zeros((B, 1, N, P), device="cuda")
+    for T in (1, 3):
+        i, Ms = ssm_inputs(gen(43), (B, T), 1, 1, N, P, torch.bfloat16, False, True, 1)
+        M[-1:] = Ms
+        y = sdm.sdm_ssm_forward(M=M, init="continue", **i)
+        own = {n: (x[-1:].contiguous() if n in ("k", "q", "v", "dt") else x) for n, x in i.items()}
+        yo = sdm.sdm_ssm_forward(M=Ms, init="continue", **own)
+        assert torch.equal(y[-1:], yo) and torch.equal(M[-1:], Ms)
+    M[-1:] = Ms
+    one = {n: (x[:, 0].contiguous() if n in ("k", "q", "v", "dt") else x) for n, x in i.items()}
+    y = sdm.sdm_ssm_step(M=M, **one)
+    own = {n: (x[-1:].contiguous() if n in ("k", "q", "v", "dt") else x) for n, x in one.items()}
+    yo = sdm.sdm_ssm_step(M=Ms, **own)
+    assert torch.equal(y[-1:], yo) and torch.equal(M[-1:], Ms)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
