@@ -572,18 +572,18 @@ def _pitch(t, name, shape, lead, dtype, dev):
         if shape[i] != 1 and st[i] != width:
             raise ValueError(f"{name}: a token's values must be contiguous")
         width *= shape[i]
-    pitch, rows = 0, 1
+    pitch, rows = None, 1
     for i in range(lead - 1, -1, -1):
         if shape[i] == 1:
             continue
-        if pitch == 0:
+        if pitch is None:
             pitch = st[i]
+            if pitch < width:  # 0 where the rows are broadcast
+                raise ValueError(f"{name}: rows overlap")
         elif st[i] != rows * pitch:
             raise ValueError(f"{name}: the rows of its sequences must follow one another")
         rows *= shape[i]
-    if rows > 1 and pitch < width:
-        raise ValueError(f"{name}: rows overlap")
-    return pitch if rows > 1 else 0
+    return 0 if pitch is None else pitch
 
 
 def _cuda(t, name):
