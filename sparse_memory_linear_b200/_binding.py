@@ -503,7 +503,10 @@ def _scope(stream, dev):
     """The given stream (a torch stream or a raw handle) as the current one of the tensors' device:
     what a call allocates then belongs to the stream that it runs on."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        handle = int(stream)
+        # torch takes a null handle as none given, and would return a stream of its pool
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle \
+            else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
 
 

@@ -1,0 +1,80 @@
+"""How the dense-state layer's calls are made on the GPU: streams by handle, large and small
+batches, refusals before any launch."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def sdm():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import sparse_memory_linear_b200 as m
+    torch.cuda.set_device(0)
+    yield m
+    torch.cuda.synchronize()
+    assert m.sdm_get_device_status() == 0
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def randn(g, *shape, dtype=torch.float32, by=1.0):
+    return (torch.randn(*shape, generator=g, device=DEV) * by).to(dtype)
+
+
+def ssm_inputs(g, lead, H, G, N, P, t, B):
+    i = dict(k=randn(g, *lead, G, N, dtype=t, by=0.5), q=randn(g, *lead, G, N, dtype=t, by=0.5),
+             v=randn(g, *lead, H, P, dtype=t), dt=randn(g, *lead, H, dtype=t),
+             A=-(0.5 + 15 * torch.rand(H, generator=g, device=DEV)),
+             dt_bias=randn(g, H, by=0.5) - 3.0, D=randn(g, H))
+    return i, randn(g, B, H, N, P)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_null_handle_is_the_default_stream(sdm, side):
+    """stream=0, the handle of the default stream, orders a call behind that stream's work (whether
+    or not it is the current one) and that stream's work behind the call."""
+    g = gen(1)
+    i, M = ssm_inputs(g, (2, 60), 2, 1, 64, 64, BF, 2)
+    x, w = randn(g, 2, 60, 64, dtype=BF), randn(g, 64, 4)
+    state, u, r = randn(g, 2, 3, 64, dtype=BF), randn(g, 60, 256, dtype=BF), randn(g, 60, 256)
+    default = torch.cuda.default_stream()
+    assert default.cuda_stream == 0
+
+    def calls(states, **kw):
+        Ms, Mt, cs, ct = states
+        tok = {n: (t[:, 3] if n in ("k", "q", "v", "dt") else t) for n, t in i.items()}
+        return [sdm.sdm_conv_forward(x, w, cs, init="continue", **kw),
+                sdm.sdm_conv_step(x[:, 3], w, ct, **kw),
+                sdm.sdm_ssm_forward(M=Ms, init="continue", **i, **kw),
+                sdm.sdm_ssm_step(M=Mt, **tok, **kw), *sdm.sdm_block_norm(u, r, **kw), *states]
+
+    def states():
+        return [M.clone(), M.clone(), state.clone(), state.clone()]
+
+    want = calls(states())
+    live = list(i.values()) + [x, u, r]
+    kept = [t.clone() for t in live]
+    for t in live:
+        t.zero_()
+    new = states()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream() if side else default):
+        with torch.cuda.stream(default):
+            torch.cuda._sleep(20_000_000)  # about 10 ms, and only then the inputs
+            for t, src in zip(live, kept):
+                t.copy_(src)
+        got = calls(new, stream=0)
+        with torch.cuda.stream(default):
+            got = [t.clone() for t in got]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
