@@ -507,6 +507,8 @@ def _scope(stream, dev):
         # torch takes a null handle as none given, and would return a stream of its pool
         stream = torch.cuda.ExternalStream(handle, device=dev) if handle \
             else torch.cuda.default_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
     return torch.cuda.stream(stream)
 
 

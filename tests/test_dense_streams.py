@@ -53,3 +53,10 @@ def test_handles_and_streams_are_used_as_given(used):
         pass
     assert used[0] is own
     assert used[1].cuda_stream == 1234 and used[1].device == DEV
+
+
+def test_streams_of_another_device_are_refused(used):
+    """The call would run on the current stream of its tensors' device, not on the given one."""
+    with pytest.raises(ValueError):
+        b._scope(Stream(77, torch.device("cuda", 0)), DEV)
+    assert not used
