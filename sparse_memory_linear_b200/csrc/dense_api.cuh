@@ -211,9 +211,10 @@ bool tile_map(CUtensorMap* map, const void* p, int width, int heads, long long r
 // the same for one token as for 128, the token-by-token scan about 0.27 us a token.  Measured
 // (us, N = 128): 8 heads of 64, 16 tokens 9.7 against 7.2 token by token, 32 tokens 9.5 against
 // 11.7; 8 x 32 heads of 64, 16 tokens 16.2 against 16.3, 32 tokens 16.3 against 27.1.
+// Its row numbers are 32 bits wide and, in the last block, reach SB_L - 1 rows behind the batch.
 bool ssm_block_fits(const sdm_ssm_shape& s, bool packed) {
   const long long rows = packed ? s.T : (long long)s.B * s.T, length = packed ? s.T / s.B : s.T;
-  return s.in_dtype == SDM_BF16 && s.N <= 128 && length >= 24 && rows < 2147483647LL;
+  return s.in_dtype == SDM_BF16 && s.N <= 128 && length >= 24 && rows <= 2147483647LL - SB_L;
 }
 
 // How a scan cuts sequences into segments.  A CTA walks a segment `unit` rows at a time in about
