@@ -137,16 +137,21 @@ def normal_f64(seed: int, tid: int, start: int, count: int, device) -> torch.Ten
 
 
 def draw(seed: int, tid: int, shape, dtype: torch.dtype, device="cpu", scale: float = 1.0,
-         transform=None, chunk: int = 1 << 24) -> torch.Tensor:
+         transform=None, chunk: int | None = None) -> torch.Tensor:
     """A tensor of ``shape`` filled element-by-element (row-major order) from the stream.
 
     transform(z, flat_index) may map the float64 draws before rounding to ``dtype``.
+    chunk: elements made at a time; no value depends on it.  By default 2^24 on a GPU, and on
+    the CPU 2^15 for each of torch's threads, whose share of every step then stays in its
+    cache (2^25 values on 8 threads: 0.5 s, and 3 s in pieces of 2^24).
     """
     shape = tuple(int(s) for s in shape)
     n = 1
     for s in shape:
         n *= s
     out = torch.empty(n, dtype=dtype, device=device)
+    if chunk is None:
+        chunk = 1 << 24 if out.is_cuda else torch.get_num_threads() << 15
     for s0 in range(0, n, chunk):
         c = min(chunk, n - s0)
         z = normal_f64(seed, tid, s0, c, device)
