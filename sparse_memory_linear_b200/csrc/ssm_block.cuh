@@ -360,8 +360,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + SB_TMEM_PTR);
-  // use: how many times the barrier completed before
-  auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u); };
+  // use: how many times the barrier completed before; by a whole warp, or by a lane of its own
+  auto wait = [&](int i, int use) { return mbar_wait_warp(bar(i), (uint32_t)use & 1u); };
+  auto wait_lane = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u); };
   auto prep = [&](int c) {
     return reinterpret_cast<SsmPrep*>(sm + SB_PREP + (c & 3) * sizeof(SsmPrep));
   };
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
     if (elect_one()) mma_commit(bar(BAR_DRAIN));
     __syncwarp();
-    ok = mbar_wait(bar(BAR_DRAIN), 0) && ok;
+    ok = mbar_wait_warp(bar(BAR_DRAIN), 0) && ok;
   } else if (warp == 17) {
     // ------------------------------------------------ products dM, part onto part, and Y1
     constexpr uint32_t dM = mma_desc(128, 64, 1, 1), dY1 = mma_desc(128, 64, 0, 1);
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
     if (elect_one()) mma_commit(bar(BAR_DRAIN + 1));
     __syncwarp();
-    ok = mbar_wait(bar(BAR_DRAIN + 1), 0) && ok;
+    ok = mbar_wait_warp(bar(BAR_DRAIN + 1), 0) && ok;
   } else if (warp == 19) {
     // ------------------------------------------------ loads of k and q
     int kc = 0, qc = 0;  // blocks whose load is issued
@@ -804,14 +805,14 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         for (int c = u0; c < u0 + w.nb; ++c) {
           const uint32_t stage = c & 1;
           const int r = w.row0 + (c - u0) * SB_L;
-          ok = c < 2 || wait(BAR_KFREE + stage, (c >> 1) - 1);
+          ok = c < 2 || wait_lane(BAR_KFREE + stage, (c >> 1) - 1);
           if (!ok) break;
           mbar_expect(bar(BAR_KFULL + stage), npanels * SB_PANEL);
           for (int pl = 0; pl < npanels; ++pl)
             tma_load_3d(base + SB_K + (2 * stage + pl) * SB_PANEL, &ba.mk, 64 * pl, g, r,
                         bar(BAR_KFULL + stage));
           kc = c + 1;
-          ok = c < 1 || wait(BAR_QFREE, c - 1);
+          ok = c < 1 || wait_lane(BAR_QFREE, c - 1);
           if (!ok) break;
           mbar_expect(bar(BAR_QFULL), npanels * SB_PANEL);
           for (int pl = 0; pl < npanels; ++pl)
@@ -848,13 +849,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         for (int c = u0; c < u0 + w.nb; ++c) {
           const uint32_t slot = c & 3;
           const int r = w.row0 + (c - u0) * SB_L;
-          ok = c < 4 || wait(BAR_PREPFREE + slot, (c >> 2) - 1);
+          ok = c < 4 || wait_lane(BAR_PREPFREE + slot, (c >> 2) - 1);
           if (!ok) break;
           mbar_expect(bar(BAR_PREP + slot), sizeof(SsmPrep));
           bulk_load(base + SB_PREP + slot * sizeof(SsmPrep), from + (size_t)(c - u0) * a.H,
                     sizeof(SsmPrep), bar(BAR_PREP + slot));
           pc = c + 1;
-          ok = c < 4 || wait(BAR_VFREE + slot, (c >> 2) - 1);
+          ok = c < 4 || wait_lane(BAR_VFREE + slot, (c >> 2) - 1);
           if (!ok) break;
           mbar_expect(bar(BAR_VFULL + slot), SB_PANEL);
           tma_load_3d(base + SB_V + slot * SB_PANEL, &ba.mv, w.p0, w.h, r, bar(BAR_VFULL + slot));
@@ -938,7 +939,8 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + SG_TMEM_PTR);
-  auto wait = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u); };
+  auto wait = [&](int i, int use) { return mbar_wait_warp(bar(i), (uint32_t)use & 1u); };
+  auto wait_lane = [&](int i, int use) { return mbar_wait(bar(i), (uint32_t)use & 1u); };
   auto prep = [&](int stage) {
     return reinterpret_cast<const SsmPrep*>(sm + SG_PREP + stage * sizeof(SsmPrep));
   };
@@ -1048,7 +1050,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
     }
     if (elect_one()) mma_commit(bar(GB_DRAIN));
     __syncwarp();
-    ok = mbar_wait(bar(GB_DRAIN), 0) && ok;
+    ok = mbar_wait_warp(bar(GB_DRAIN), 0) && ok;
   } else {
     int stage = 0, round = 0, n = 0;
     while (next_piece()) {
@@ -1058,7 +1060,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
         const int g = w.h / (a.H / a.G);
         for (int c = 0; c < nb; ++c) {
           const int at = nb - 1 - c, r = w.row0 + at * SB_L;
-          ok = n < SG_STAGES || wait(GB_FREE + stage, round - 1);
+          ok = n < SG_STAGES || wait_lane(GB_FREE + stage, round - 1);
           if (!ok) break;
           mbar_expect(bar(GB_FULL + stage), (npanels + 1) * SB_PANEL + sizeof(SsmPrep));
           bulk_load(base + SG_PREP + stage * sizeof(SsmPrep), from + (size_t)at * a.H,

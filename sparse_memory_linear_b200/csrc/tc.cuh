@@ -22,10 +22,12 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// Every wait ends: a try suspends the thread for up to two microseconds, and after 2^20 of them
-// (seconds, against microseconds in a sound run) the wait gives up and the caller leaves its
+// Every wait ends: a try suspends the thread for up to two microseconds, and after TRIES of them
+// (2^20: seconds, against microseconds in a sound run) the wait gives up and the caller leaves its
 // loops; the block's other waits run out in the same way, and the kernel records SDM_ERR_TIMEOUT
 // when it ends.  Kept to a few instructions: a kernel has dozens of these.
+constexpr int MBAR_TRIES = 1 << 20;
+template <int TRIES = MBAR_TRIES>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -35,12 +37,36 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
       "@p bra DONE;\n\t"
       "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 1048576;\n\t"
+      "setp.lt.u32 q, n, %3;\n\t"
       "@q bra TRY;\n"
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "n"(TRIES)
+      : "memory");
+  return ok != 0;
+}
+// The same by a whole warp, which goes on or gives up as one: behind a wait stand instructions that
+// all its lanes have to reach (tcgen05.ld, elect.sync, __syncwarp), and lanes whose tries end
+// differently at the limit would part there.  A lane that has seen the phase complete keeps
+// seeing it: no barrier completes its next phase before this warp has gone on.
+template <int TRIES = MBAR_TRIES>
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "TRY:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+      "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, %3;\n\t"
+      "@q bra TRY;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "n"(TRIES)
       : "memory");
   return ok != 0;
 }
