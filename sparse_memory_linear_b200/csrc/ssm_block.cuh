@@ -34,6 +34,8 @@
 // exceeds 1.
 #pragma once
 
+#include <cfloat>
+
 #include "ssm.cuh"
 #include "tc.cuh"
 
@@ -205,7 +207,8 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, S
   const long long row0 = seq0 + ((long long)blockIdx.x - ssm_first_block(a.seq, b)) * SB_L;
   if (row0 < seq0 || row0 >= seq1) return;
   const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt) + h;
-  const float A2 = a.A[h] * SB_LOG2E, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+  // finite where A is: a step of size 0 times infinity would be NaN
+  const float A2 = fmaxf(a.A[h] * SB_LOG2E, -FLT_MAX), bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
   float raw[4];
   bool live[4];
 #pragma unroll

@@ -78,3 +78,18 @@ def test_null_handle_is_the_default_stream(sdm, side):
             got = [t.clone() for t in got]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 9, 150])
+def test_steps_of_size_0_keep_the_state_at_any_decay_rate(sdm, dt, T):
+    """A up to the largest finite value: exp(0 A) is 1, for tokens whose dt is -infinity."""
+    i, M = ssm_inputs(gen(9), (1, T), 2, 1, 64, 64, BF if dt == "bf16" else torch.float32, 1)
+    i["A"] = torch.tensor([-torch.finfo(torch.float32).max, -2.5e38], device=DEV)
+    i["dt"][:] = float("-inf")
+    keep = M.clone()
+    y = sdm.sdm_ssm_forward(M=M, init="continue", **i)
+    assert torch.equal(M, keep) and torch.isfinite(y).all()
+    one = {n: (t[:, 0] if n in ("k", "q", "v", "dt") else t) for n, t in i.items()}
+    ys = sdm.sdm_ssm_step(M=M, **one)
+    assert torch.equal(M, keep) and torch.isfinite(ys).all()
