@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, NV == 1 ? (TPR > 256 ? 
       cur.r[i].get2(r[i]);
       if (a.gate) {
         cur.z[i].get2(z);
-        fast_act<4>(z, a.act);
+        pair_act<T, 4>(z, a.act);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

@@ -195,7 +195,7 @@ struct ConvLane {
       for (int j = 0; j < K; ++j) acc = fma2(w[j][e], win[j][e], acc);
       o[e] = acc;
     }
-    fast_act<2>(o, act);
+    pair_act<T, 2>(o, act);
 #pragma unroll
     for (int j = 0; j + 1 < K; ++j)
 #pragma unroll

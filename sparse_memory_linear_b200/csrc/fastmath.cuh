@@ -46,9 +46,10 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// act(g) from one exponential and one reciprocal of the hardware, against tens of instructions
-// for expf and a division.  The error relative to act(g) is about 2^-21 (1 + |g| / 4 for negative
-// g): far below half a step of bf16, and a few steps of fp32.
+// act(g) for values that were or will be bf16, from one exponential and one reciprocal of the
+// hardware, against tens of instructions for expf and a division.  The error relative to act(g) is
+// about 2^-21 (1 + |g| / 4) for g > -87, far below half a step of bf16, 2^-8; below that the
+// result, at most 2e-36, is 0.
 // The activation is chosen once for all of a thread's pairs: chosen value by value it cost as
 // much again.
 __device__ __forceinline__ float2 fast_sigmoid2(float2 g) {
@@ -59,14 +60,27 @@ __device__ __forceinline__ float2 fast_sigmoid2(float2 g) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
   return r;
 }
-template <int PAIRS>
-__device__ __forceinline__ void fast_act(float2 g[PAIRS], int act) {
+// For fp32 values: good to 9 half steps (expf 2 ulp, the reciprocal of a number in 1 .. 2 1 ulp),
+// and to the last denormal.  20011 x 2568 fp32 convolutions take 78.3 us, 79.5 with the short form.
+__device__ __forceinline__ float act_f32(float g, bool silu) {
+  const float e = expf(-fabsf(g));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  const float top = g < 0.0f ? e : 1.0f;
+  return (silu ? g * top : top) * r;
+}
+template <typename T, int PAIRS>
+__device__ __forceinline__ void pair_act(float2 g[PAIRS], int act) {
   if (act == SDM_GATE_IDENTITY) return;
   const bool silu = act == SDM_GATE_SILU;
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) {
-    const float2 s = fast_sigmoid2(g[i]);
-    g[i] = mul2(s, make_float2(silu ? g[i].x : 1.0f, silu ? g[i].y : 1.0f));
+    if constexpr (sizeof(T) == 2) {
+      const float2 s = fast_sigmoid2(g[i]);
+      g[i] = mul2(s, make_float2(silu ? g[i].x : 1.0f, silu ? g[i].y : 1.0f));
+    } else {
+      g[i] = make_float2(act_f32(g[i].x, silu), act_f32(g[i].y, silu));
+    }
   }
 }
 

@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             float2 g[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[j] = unpack_bf16(z[j]);
-            fast_act<8>(g, a.act);
+            pair_act<__nv_bfloat16, 8>(g, a.act);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = mul2(o[j], g[j]);
             if (part < 3) load_z(part + 1);

@@ -4,6 +4,8 @@ batches, refusals before any launch."""
 import pytest
 import torch
 
+from tests import _dense as ref
+
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
@@ -93,3 +95,25 @@ def test_steps_of_size_0_keep_the_state_at_any_decay_rate(sdm, dt, T):
     one = {n: (t[:, 0] if n in ("k", "q", "v", "dt") else t) for n, t in i.items()}
     ys = sdm.sdm_ssm_step(M=M, **one)
     assert torch.equal(M, keep) and torch.isfinite(ys).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_activations_of_fp32_values(sdm, act):
+    """Relative to the result, at large negative arguments too: with e = e^-|x| by expf (2 ulp, 4 U),
+    1 + e (U), its reciprocal (1 ulp, 2 U) and two products (2 U) 9 U, and 2 ulp of a denormal e
+    times |x| and three roundings of denormals."""
+    x = torch.cat([torch.linspace(-95, 95, 40000, device=DEV),
+                   randn(gen(3), 960)]).reshape(1, -1, 64).contiguous()
+    want = ref.act64(x.double(), act)
+    lim = 9 * ref.U * want.abs() + 100 * 2.0 ** -148
+    w = torch.zeros(64, 4, device=DEV)
+    w[:, 3] = 1.0  # a sum of one term: the activation's argument is exact
+    state = torch.zeros(1, 3, 64, device=DEV)
+    for y in (sdm.sdm_conv_forward(x, w, act=act),
+              sdm.sdm_block_norm(torch.ones_like(x), torch.zeros_like(x), post_norm=False, gate=x,
+                                 act=act, want_n=False)[0],
+              torch.cat([sdm.sdm_conv_step(x[:, t], w, state, act=act) for t in range(40)], 0)):
+        y = y.double().reshape(-1, 64)
+        n = y.shape[0]
+        err = (y - want.reshape(-1, 64)[:n]).abs()
+        assert (err <= lim.reshape(-1, 64)[:n]).all(), (err / lim.reshape(-1, 64)[:n]).max()
