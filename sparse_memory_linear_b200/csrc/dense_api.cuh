@@ -229,7 +229,8 @@ struct SsmCost {
 };
 
 struct SsmPlan {
-  long long seg_rows, items;  // rows of a segment; (sequence, segment) pairs at most
+  // rows of a segment; (sequence, segment) pairs, and segments of split sequences, at most
+  long long seg_rows, items, slots;
   bool split;
   size_t off_decays, off_prep, off_items, bytes;
 };
@@ -258,8 +259,11 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, long long ctas_per_item, c
   p.items = packed ? s.T / p.seg_rows + s.B
                    : s.B * (s.T > 0 ? (s.T + p.seg_rows - 1) / p.seg_rows : 1);
   if (p.split) {
-    p.off_decays = round_up((size_t)p.items * s.H * s.N * s.d_v * 4, WS_ALIGN);
-    p.bytes = p.off_decays + round_up((size_t)p.items * s.H * 4, WS_ALIGN);
+    // a packed sequence of n > seg_rows rows has at most 2 n / seg_rows segments
+    p.slots = p.items;
+    if (packed && 2LL * s.T / p.seg_rows < p.slots) p.slots = 2LL * s.T / p.seg_rows;
+    p.off_decays = round_up((size_t)p.slots * s.H * s.N * s.d_v * 4, WS_ALIGN);
+    p.bytes = p.off_decays + round_up((size_t)p.slots * s.H * 4, WS_ALIGN);
   }
   return p;
 }
@@ -284,7 +288,7 @@ SsmPlan ssm_plan(const sdm_ssm_shape& s, bool packed, int sms, bool block) {
 }
 
 SsmSplit ssm_split(const SsmPlan& plan, void* ws) {
-  return SsmSplit{plan.seg_rows, plan.items, static_cast<float*>(ws),
+  return SsmSplit{plan.seg_rows, plan.items, plan.slots, static_cast<float*>(ws),
                   reinterpret_cast<float*>(static_cast<char*>(ws) + plan.off_decays)};
 }
 

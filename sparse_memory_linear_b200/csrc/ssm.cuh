@@ -49,9 +49,11 @@ __device__ __forceinline__ float ssm_step_size(float dt, int softplus) {
 }
 
 // The (sequence, segment) of work item `item`: a sequence of n rows has max(1, ceil(n / seg))
-// segments.  Called by one warp; false past the last.
+// segments.  *slot: its number among the segments of the sequences that have several, which
+// only these use.  Called by one warp; false past the last.
 __device__ __forceinline__ bool ssm_find_item(const SeqBounds& seq, long long item, long long seg,
-                                              int* b_out, long long* s_out) {
+                                              int* b_out, long long* s_out, long long* slot) {
+  *slot = item;
   if (!seq.cu) {
     const long long per = seq.T > 0 ? (seq.T + seg - 1) / seg : 1;
     *b_out = (int)(item / per);
@@ -73,13 +75,16 @@ __device__ __forceinline__ bool ssm_find_item(const SeqBounds& seq, long long it
       if (lane >= s) upto += o;
     }
     const unsigned hit = __ballot_sync(FULL_MASK, upto > item);
+    const unsigned whole = __ballot_sync(FULL_MASK, n == 1);
     if (hit) {
       const int l = __ffs(hit) - 1;
+      *slot -= __popc(whole & ((1u << l) - 1));
       *b_out = b0 + l;
       *s_out = item - __shfl_sync(FULL_MASK, upto - n, l);
       return true;
     }
     item -= __shfl_sync(FULL_MASK, upto, 31);
+    *slot -= __popc(whole);
   }
   return false;
 }
@@ -89,9 +94,15 @@ __device__ __forceinline__ bool ssm_find_item(const SeqBounds& seq, long long it
 // segments turns those into the states before them, and the scan starts from these.
 struct SsmSplit {
   long long seg_rows;  // rows of a segment
-  long long items;     // places for segments' states; only bad offsets ask for more
-  float* starts;       // [items, H, N, P]: the state before each segment of a split sequence
-  float* decays;       // [items, H]: the segment's whole decay
+  long long items;     // (sequence, segment) pairs; only bad offsets make up more
+  long long slots;     // segments of split sequences, likewise; 0 where none is split
+  float* starts;       // [slots, H, N, P]: the state before each segment of a split sequence
+  float* decays;       // [slots, H]: the segment's whole decay
+
+  // The place of a segment's state: in range whatever bad offsets make up.
+  __device__ __forceinline__ long long place(long long slot) const {
+    return slot < slots ? slot : slots > 0 ? slots - 1 : 0;
+  }
 };
 
 // Token-by-token scan.  A block holds 16 of a head's d_v columns: four per warp, eight lanes to
@@ -126,7 +137,7 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
   __shared__ __align__(16) T sv[2][TB][SSM_COLS], sz[2][TB][SSM_COLS];
   __shared__ float sy[2][TB][SSM_COLS], sd[2][TB], sa[2][TB];
   __shared__ int s_ok, s_b;
-  __shared__ long long s_seg;
+  __shared__ long long s_seg, s_slot;
   const int tid = threadIdx.x, lane = tid & 31, ln = lane & 7;
   const int col = (tid >> 5) * 4 + (lane >> 3);
   const int h = blockIdx.y, g = h / (a.H / a.G);
@@ -134,12 +145,13 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
   if (!CONTRIB && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.seq.check();
   if (tid < 32) {
     int b = 0;
-    long long seg = 0;
-    const bool ok = ssm_find_item(a.seq, blockIdx.x, sp.seg_rows, &b, &seg);
+    long long seg = 0, slot = 0;
+    const bool ok = ssm_find_item(a.seq, blockIdx.x, sp.seg_rows, &b, &seg, &slot);
     if (tid == 0) {
       s_ok = ok;
       s_b = b;
       s_seg = seg;
+      s_slot = sp.place(slot);
     }
   }
   // columns of rows that do not exist stay 0
@@ -154,11 +166,12 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
   __syncthreads();
   if (!s_ok) return;
   const int b = s_b;
+  const long long slot = s_slot;
   const long long seq0 = a.seq.start(b), seq1 = a.seq.end(b), r0 = seq0 + s_seg * sp.seg_rows;
   const long long r1 = r0 + sp.seg_rows < seq1 ? r0 + sp.seg_rows : seq1;
   const bool split = seq1 - seq0 > sp.seg_rows;
   // nothing follows the last segment; no place for what bad offsets make up
-  if (CONTRIB && (r1 == seq1 || blockIdx.x + 1 >= sp.items)) return;
+  if (CONTRIB && (r1 == seq1 || slot + 1 >= sp.slots)) return;
   const T* kp = static_cast<const T*>(a.k) + (size_t)g * a.N;
   const T* qp = static_cast<const T*>(a.q) + (size_t)g * a.N;
   const T* vp = static_cast<const T*>(a.v) + (size_t)h * a.P + p0;
@@ -168,8 +181,8 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
   const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f, D = a.D ? a.D[h] : 0.0f;
   float* Mp = a.M + ((size_t)b * a.H + h) * a.N * a.P;
   const float* from =
-      split ? sp.starts + ((size_t)blockIdx.x * a.H + h) * a.N * a.P : Mp;
-  float* to = CONTRIB ? sp.starts + ((size_t)(blockIdx.x + 1) * a.H + h) * a.N * a.P : Mp;
+      split ? sp.starts + ((size_t)slot * a.H + h) * a.N * a.P : Mp;
+  float* to = CONTRIB ? sp.starts + ((size_t)(slot + 1) * a.H + h) * a.N * a.P : Mp;
   float s[NJ][4];
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
@@ -297,7 +310,7 @@ __global__ void __launch_bounds__(128) ssm_scan_kernel(SsmArgs a, SsmSplit sp) {
   if (CONTRIB && p0 == 0 && tid < 32) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) decay += __shfl_xor_sync(FULL_MASK, decay, m);
-    if (tid == 0) sp.decays[(size_t)blockIdx.x * a.H + h] = expf(decay);
+    if (tid == 0) sp.decays[(size_t)slot * a.H + h] = expf(decay);
   }
 }
 
@@ -335,11 +348,14 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) 
       __syncthreads();
       if (a.seq.cu) {
         unsigned long long items = 0;
-        for (int i = threadIdx.x; i < b; i += 256) items += items_of(i);
+        for (int i = threadIdx.x; i < b; i += 256) {
+          const long long n = items_of(i);
+          if (n > 1) items += n;
+        }
         if (items) atomicAdd(&s_first, items);
       }
       __syncthreads();
-      const long long first = (long long)s_first, room = sp.items - first;
+      const long long first = (long long)s_first, room = sp.slots - first;
       const int segs = (int)(items_of(b) < room ? items_of(b) : room);
       if (segs <= 0) continue;
       for (int unit = mine0; unit < units; unit += grid) {

@@ -89,7 +89,7 @@ struct SsmBlockArgs {
   SsmSplit sp;      // segments of whole blocks
   SsmPrep* prep;    // [blocks, H]
   int4* items;      // [items] (sequence, its first and past-last row, the segment's first row),
-                    // longest first, then [items] ints: each one's number among the items
+                    // longest first, then [items] ints: the place of each one's state (SsmSplit)
   int ptiles;       // 64-column tiles of d_v
   int step_items, step_parts;  // gridDim.x = step_items x (H x ptiles) + step_parts
 };
@@ -158,8 +158,8 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, S
     const int item = ((int)blockIdx.x - blocks) * 8 + warp;
     if (blockIdx.y != 0 || item >= n_items) return;
     int b = 0;
-    long long seg = 0;
-    const bool ok = ssm_find_item(a.seq, item, sp.seg_rows, &b, &seg);
+    long long seg = 0, slot = 0;
+    const bool ok = ssm_find_item(a.seq, item, sp.seg_rows, &b, &seg, &slot);
     // Longest first: CTAs that walk every gridDim.x-th piece then end at about the same time.  The
     // place is the number of longer items and of equal ones before (bad offsets can make up
     // more items than there are places: their order is left alone).
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmArgs a, SsmSplit sp, S
       items[place] = ok ? make_int4(b, (int)a.seq.start(b), (int)a.seq.end(b),
                                     (int)(a.seq.start(b) + seg * sp.seg_rows))
                         : make_int4(-1, 0, 0, 0);
-      reinterpret_cast<int*>(items + n_items)[place] = item;
+      reinterpret_cast<int*>(items + n_items)[place] = (int)sp.place(slot);
     }
     return;
   }
@@ -273,7 +273,7 @@ __device__ __forceinline__ void ssm_store_parts(uint8_t* place, uint32_t o0, uin
 // walks every gridDim.x-th piece.
 struct SsmPiece {
   int place, part;  // place in the list of work items, and part: head + H x tile
-  int item, b, seq0, seq1, row0, row1, h, p0, nb;  // nb blocks
+  int slot, b, seq0, seq1, row0, row1, h, p0, nb;  // slot: of its state; nb blocks
   __device__ __forceinline__ void begin(const SsmBlockArgs& ba) {
     const int parts = ba.a.H * ba.ptiles;
     place = (int)blockIdx.x / parts;
@@ -290,7 +290,7 @@ struct SsmPiece {
       h -= H;
       p0 += SB_P;
     }
-    item = __ldg(reinterpret_cast<const int*>(ba.items + ba.sp.items) + place);
+    slot = __ldg(reinterpret_cast<const int*>(ba.items + ba.sp.items) + place);
     b = at.x;
     seq0 = at.y;
     seq1 = at.z;
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       float* const mrow = a.M + (((size_t)w.b * a.H + w.h) * a.N + n) * a.P + w.p0;
       const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
       const float* const from =
-          split ? ba.sp.starts + (((size_t)w.item * a.H + w.h) * a.N + n) * a.P + w.p0 : mrow;
+          split ? ba.sp.starts + (((size_t)w.slot * a.H + w.h) * a.N + n) * a.P + w.p0 : mrow;
 #pragma unroll
       for (int i = 0; i < SB_P; i += 4) {
         float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       // the piece, and block by block the gate
       const bool split = w.seq1 - w.seq0 > ba.sp.seg_rows;
       if (w.nb > 0 && (split || !a.from_zero)) {
-        const float* m = (split ? ba.sp.starts + ((size_t)w.item * a.H + w.h) * a.N * a.P
+        const float* m = (split ? ba.sp.starts + ((size_t)w.slot * a.H + w.h) * a.N * a.P
                                 : a.M + ((size_t)w.b * a.H + w.h) * a.N * a.P) + w.p0;
         const int bytes = 4 * (a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P);
         for (int n = lane; n < a.N; n += 32)
@@ -958,7 +958,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
     if (turn >= 0) w.advance(ba);
     ++turn;
     for (; ok && w.get(ba); w.advance(ba))
-      if (w.row1 < w.seq1 && w.item + 1 < ba.sp.items) return true;
+      if (w.row1 < w.seq1 && w.slot + 1 < ba.sp.slots) return true;
     return false;
   };
 
@@ -994,7 +994,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
           ++round;
         }
       }
-      if (tid == 0 && w.p0 == 0) ba.sp.decays[(size_t)w.item * a.H + w.h] = exp2f(carry);
+      if (tid == 0 && w.p0 == 0) ba.sp.decays[(size_t)w.slot * a.H + w.h] = exp2f(carry);
       if (warp < 4 && ok) {
         ok = wait(GB_DONE, turn);
         if (!ok) break;
@@ -1002,7 +1002,7 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
         const int n = tid, pn = a.P - w.p0 < SB_P ? a.P - w.p0 : SB_P;
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         // the state before the next segment gets this one's contribution
-        float* to = ba.sp.starts + (((size_t)(w.item + 1) * a.H + w.h) * a.N + n) * a.P + w.p0;
+        float* to = ba.sp.starts + (((size_t)(w.slot + 1) * a.H + w.h) * a.N + n) * a.P + w.p0;
 #pragma unroll
         for (int part = 0; part < 4; ++part) {
           float r1[16], r2[16];

@@ -33,3 +33,17 @@ def test_block_wise_scan_keeps_its_row_numbers_in_32_bits(sdm, B):
             T += 1        # B T rows are then past the limit, and the packed reading too small
         got = scratch(sdm, B, T)
         assert (got >= rows // L * SUMS) == blocks, rows
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("B,T,H,P", [(1024, 8192, 32, 128), (4096, 512, 8, 64), (60000, 30, 4, 32),
+                                     (512, 8192, 64, 64)])
+def test_scratch_does_not_grow_with_the_states_of_whole_sequences(sdm, bf16, B, T, H, P):
+    """Batches with enough sequences to fill the device are not cut into segments; read as packed
+    (the size serves both), only sequences of several segments need room for states, two for
+    every segment's worth of rows at most.  What is left are the blocks' sums and the items."""
+    N = 128
+    states = B * H * N * P * 4
+    blocks = max(B * -(-T // L), T // L + B + 1) if bf16 else 0
+    need = scratch(sdm, B, T, H, 1, N, P, bf16)
+    assert need - blocks * H * SUMS - 20 * (blocks + B) <= states / 8

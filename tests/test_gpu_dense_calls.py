@@ -1,6 +1,8 @@
 """How the dense-state layer's calls are made on the GPU: streams by handle, large and small
 batches, refusals before any launch."""
 
+import random
+
 import pytest
 import torch
 
@@ -117,3 +119,35 @@ def test_activations_of_fp32_values(sdm, act):
         n = y.shape[0]
         err = (y - want.reshape(-1, 64)[:n]).abs()
         assert (err <= lim.reshape(-1, 64)[:n]).all(), (err / lim.reshape(-1, 64)[:n]).max()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_packed_batches_of_many_sequences(sdm, dt):
+    """More sequences than the 32 that a warp looks at together and the 256 that a block does, the
+    ones that are cut into segments among the first and behind both."""
+    g = random.Random(4)
+    lens = [g.randint(0, 40) for _ in range(300)]
+    lens[5], lens[40], lens[290], lens[299] = 700, 1500, 2600, 0
+    B, H, G, N, P, n = len(lens), 2, 1, 32, 24, sum(lens)
+    assert n // B >= 24
+    t = BF if dt == "bf16" else torch.float32
+    i, M = ssm_inputs(gen(5), (n + 7,), H, G, N, P, t, B)
+    cu = torch.tensor([sum(lens[:b]) for b in range(B + 1)], dtype=torch.int32, device=DEV)
+    M0, y = M.double(), torch.full_like(i["v"], 7.0)
+    sdm.sdm_ssm_forward(M=M, init="continue", cu=cu, y=y, **i)
+    f = {k: x.double()[:n] if k in ("k", "q", "v", "dt") else x.double() for k, x in i.items()}
+    ry, rM, yb, Mb = ref.ssm(f["k"], f["q"], f["v"], f["dt"], f["A"], M0, f["D"], f["dt_bias"],
+                             True, None, "silu", lens,
+                             weights=2.0 ** -8 + 2.0 ** -16 if dt == "bf16" else 0.0)
+    ref.check(y[:n], ry, yb, "y")
+    ref.check(M, rM, Mb, "M")
+    assert (y[n:] == 7).all()
+    # the convolution of the same rows
+    C = H * P
+    x, w, state = i["v"].flatten(1)[:n].contiguous(), randn(gen(6), C, 4), \
+        randn(gen(7), B, 3, C, dtype=t)
+    s0 = state.double()
+    yc = sdm.sdm_conv_forward(x, w, state, init="continue", cu=cu)
+    rc, rs, bound = ref.conv(x.double(), w.double(), None, s0, "silu", lens)
+    ref.check(yc, rc, bound, "y")
+    assert torch.equal(state.double(), rs)
