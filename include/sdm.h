@@ -357,7 +357,8 @@ typedef struct {
  * state [B,K-1,C] in_dtype, a sequence's last K - 1 inputs, oldest first: SDM_CONTINUE reads
  * it as the inputs before the first token, SDM_INIT_ZERO takes those as zero (state may then
  * be NULL: not kept); it is rewritten with the last K - 1 inputs seen (an empty sequence
- * keeps its state, or gets zeros with SDM_INIT_ZERO).  One launch.
+ * keeps its state, or gets zeros with SDM_INIT_ZERO).  Sums are fp32; act() is good to a few ulp
+ * of fp32 for fp32 channels and to 2^-21 (1 + |g| / 4) for bf16 ones.  One launch.
  */
 sdm_status sdm_conv_forward(const void *x, const float *w, const float *bias, void *state,
                             int32_t init, int32_t act, const int32_t *cu, void *y,
@@ -397,6 +398,12 @@ size_t sdm_ssm_workspace_size(sdm_ssm_shape shape);
  * k, q, v and dt have to be finite: a NaN or infinity also reaches other tokens of its sequence
  * (never another sequence).  Only dt may be -infinity: it, or a type's lowest value, is a step of
  * size 0, and the token (padding, for instance) leaves the state as it is.
+ * What is held in less than fp32: y, rounded once to in_dtype, and for bf16 inputs with N <= 128
+ * and sequences of 24 tokens or more (on average, when packed), which are scanned in blocks of
+ * 128 tokens counted from a sequence's first, two things that y reads: the weight
+ * d exp(...) (q . k) of a token of the same block is rounded to bf16 (half a step 2^-8, as y's own
+ * rounding), and the state before the block is read to 16 bits (2^-16).  M itself is fp32 in
+ * every form, and its sums are.  act() of a bf16 gate is good to 2^-21 (1 + |g| / 4).
  */
 sdm_status sdm_ssm_forward(const void *k, const void *q, const void *v, const void *dt,
                            const float *A, const float *dt_bias, const float *D, float *M,
@@ -421,7 +428,9 @@ sdm_status sdm_ssm_step(const void *k, const void *q, const void *v, const void 
  *   n = r_out * rsqrt(mean(r_out^2) + eps) * pre_gamma     (of the unrounded r_out)
  * u (the block's output), gate, n in in_dtype; r, r_out (the residual stream) in r_dtype;
  * post_gamma, scale, pre_gamma [D] fp32, nullable (1); n nullable (not computed).  r_out may be
- * r and n may be u or gate (the same pointer).  eps >= 0.  One launch.
+ * r and n may be u or gate (the same pointer).  eps >= 0.  Sums, means and roots are fp32; act()
+ * is good to a few ulp of fp32 for an fp32 gate and to 2^-21 (1 + |g| / 4) for a bf16 one, in
+ * an fp32 r_out as well.  One launch.
  */
 sdm_status sdm_block_norm(const void *u, const void *gate, int32_t act, int32_t post_norm,
                           const float *post_gamma, const float *scale, const void *r,

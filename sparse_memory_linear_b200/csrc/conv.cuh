@@ -6,9 +6,10 @@
 // zero.
 //
 // Bound by its bytes, every input read and every output written once.  Measured on one B200:
-// 4 x 8192 x 1280 bf16, K = 4, SiLU 35.7 us (4.70 TB/s, 0.72 of the measured copy rate; without
-// the activation 33 us; a plain copy of x 28.8 us), 20011 x 2568 fp32 in 23 packed sequences 79 us
-// (5.2 TB/s, 0.79).
+// 4 x 8192 x 1280 bf16, K = 4, SiLU 36.0 us (4.66 TB/s, 0.71 of the measured copy rate; without
+// the activation 33 us; a plain copy of x 28.8 us: a thread loads a group of rows and computes it in
+// turn, with no load on its way meanwhile), 20011 x 2568 fp32 in 23 packed sequences 79 us
+// (5.2 TB/s, 0.80).
 #pragma once
 
 #include "fastmath.cuh"

@@ -1,5 +1,6 @@
-// ssm.cuh -- selective state-space scan, the dense counterpart of the sparse memory pass: every
-// head keeps a state of N rows of d_v values that every token decays, writes and reads whole.
+// ssm.cuh -- selective state-space scan: every head keeps a state of N rows of d_v values that
+// every token decays, adds to and reads whole (the sparse memory pass touches a few rows, and
+// writes by a delta rule, with a prediction taken off; here nothing is).
 //
 // Token t of a sequence, head h (group g = h / (H / G) of the H / G heads that share k and q):
 //   d = softplus(dt[t, h] + dt_bias[h])        (or dt itself)
@@ -396,8 +397,8 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(SsmArgs a, SsmSplit sp) 
 // groups side by side, each thread eight of its rows at a time, all on their way before the
 // first is used (with a load after each store the compiler must keep them in order, and two
 // loads a thread were in flight).  The row groups' shares of the read meet in shared memory.
-// Bound by the state's bytes, read and written once: 64 x 64 heads of 128 x 64 take 44.5 us, 6.07
-// TB/s, 0.93 of the measured copy rate.
+// Bound by the state's bytes, read and written once: 64 x 64 heads of 128 x 64 take 45.7 us, 5.9
+// TB/s, 0.90 of the measured copy rate.
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
   grid_dependency_wait();

@@ -24,9 +24,12 @@
 //   sums
 // joined by mbarriers.  A block's work is a chain of short dependent steps; with the steps on
 // warps of their own the chains of successive blocks overlap.  One group for everything took 11
-// us a block, two groups 3.5, these 2.8 (3.8 with a gate; 128 tokens, N = 128, all
-// multiprocessors busy).  The groups' instructions bound it, 9300 a block; the matrix unit is busy
-// 40 % of the time, memory less.
+// us a block, two groups 3.5, these 2.9 (3.8 with a gate; 128 tokens, N = 128, all
+// multiprocessors busy).  No unit is full at that: 46 % of the issue slots are used (9500 warp
+// instructions a block), the matrix unit 39 % of the time, memory less, and a group alone needs
+// 2200 to 2800 of a block's 5500 cycles.  What bounds it is the loop of waits from one group to the
+// next; which of them sets the period is not established (q, with its one stage, is one: the
+// load of block c + 1 waits for Y2 of block c, and S of block c + 1 for the load).
 //
 // Decays are summed within runs of 32 tokens (a warp's rows) and the runs' totals added, never as
 // differences of long sums: exp(c_t - c_s) is one exponential inside a run, and the product of
