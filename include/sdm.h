@@ -400,10 +400,10 @@ size_t sdm_ssm_workspace_size(sdm_ssm_shape shape);
  * size 0, and the token (padding, for instance) leaves the state as it is.
  * What is held in less than fp32: y, rounded once to in_dtype, and for bf16 inputs with N <= 128
  * and sequences of 24 tokens or more (on average, when packed), which are scanned in blocks of
- * 128 tokens counted from a sequence's first, two things that y reads: the weight
- * d exp(...) (q . k) of a token of the same block is rounded to bf16 (half a step 2^-8, as y's own
- * rounding), and the state before the block is read to 16 bits (2^-16).  M itself is fp32 in
- * every form, and its sums are.  act() of a bf16 gate is good to 2^-21 (1 + |g| / 4).
+ * 128 tokens counted from a sequence's first, the two things that y reads: the weight
+ * d exp(...) (q . k) of a token of the same block, and the state before the block.  Both are read
+ * to 16 bits (an error of 2^-16 of their magnitude; y's own rounding is 2^-8).  M itself is
+ * fp32 in every form, and its sums are.  act() of a bf16 gate is good to 2^-21 (1 + |g| / 4).
  */
 sdm_status sdm_ssm_forward(const void *k, const void *q, const void *v, const void *dt,
                            const float *A, const float *dt_bias, const float *D, float *M,

@@ -7,12 +7,13 @@
 // so a block is four matrix products, all on tcgen05 with fp32 sums in tensor memory:
 //   S  = q k^T                      128 x 128 x N
 //   Y2 = q M                        2 products 128 x 64 x N, M as two bf16 parts (16 bits of it)
-//   Y1 = (S o weights) v            128 x 64 x 128, weights rounded to bf16
+//   Y1 = (S o weights) v            2 products 128 x 64 x 128, weights as two bf16 parts
 //   dM = k^T (w o v)                3 products N x 64 x 128, w o v as three bf16 parts (24 bits)
 // The state is kept in fp32 registers and never rounded to less: dM has to be exact to fp32,
-// hence the three parts.  What enters y may be rounded to the type of y once: each token's
-// weight in another's read (half a step of bf16); two parts of M keep the second term below
-// that.
+// hence the three parts.  y is rounded to bf16 once, half a step of 2^-8; what it reads, each token's
+// weight in another's read and the state before the block, is held to 2^-16, so that y's error
+// is its own rounding.  (With the weights in one part the error against 64 bits was up to 1.5
+// times that of a scan in fp32, rounded once.)
 //
 // One CTA walks the blocks of its (sequence segment, head, 64 value columns) pieces in order, four
 // groups of four warps each at its own block:
@@ -72,7 +73,7 @@ constexpr uint32_t SB_BARS = SB_PREP + 4 * sizeof(SsmPrep);
 enum {
   BAR_QFULL = 0, BAR_QFREE, BAR_KFULL = 2, BAR_KFREE = 4, BAR_VFULL = 6, BAR_VFREE = 10,
   BAR_PREP = 14, BAR_PREPFREE = 18, BAR_WREADY = 22, BAR_WFREE = 24, BAR_YFREE = 26,
-  BAR_S = 28, BAR_P = 30, BAR_Y = 32, BAR_DM = 34, BAR_DMFREE = 36, BAR_Y2 = 38,
+  BAR_S = 28, BAR_P = 30, BAR_Y = 32, BAR_DM = 34, BAR_DMFREE, BAR_Y2 = 38,
   BAR_HREADY = 40, BAR_HFREE, BAR_DRAIN, BAR_COUNT = BAR_DRAIN + 2
 };
 constexpr uint32_t SB_TMEM_PTR = SB_BARS + 44 * 8;
@@ -80,9 +81,9 @@ static_assert(BAR_COUNT <= 44, "barriers");
 constexpr uint32_t SB_SMEM = SB_TMEM_PTR + 32 + 1024;      // and room to align
 static_assert(SB_SMEM <= 232448 - 64, "shared memory of a block");
 
-// Tensor memory columns: two buffers of S, whose first half becomes P and whose second half,
-// once weighed, holds Y1; two buffers each of Y2 and dM.
-constexpr uint32_t TM_S = 0, TM_Y1 = 64, TM_Y2 = 256, TM_DM = 384;
+// Tensor memory columns: two buffers of S, which becomes P in place (16 columns of S, 8 of each
+// part); one of Y1; one of dM; two of Y2.
+constexpr uint32_t TM_S = 0, TM_Y1 = 256, TM_DM = 320, TM_Y2 = 384;
 
 constexpr float SB_LOG2E = 1.4426950408889634f;
 
@@ -338,9 +339,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       mbar_init(bar(BAR_Y + i), 1);
       mbar_init(bar(BAR_Y2 + i), 1);
       mbar_init(bar(BAR_YFREE + i), 4);
-      mbar_init(bar(BAR_DM + i), 1);
-      mbar_init(bar(BAR_DMFREE + i), 4);
     }
+    mbar_init(bar(BAR_DM), 1);
+    mbar_init(bar(BAR_DMFREE), 4);
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(BAR_PREP + i), 1);
       mbar_init(bar(BAR_PREPFREE + i), 16);
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] = next[i];
           if (grp + 1 < groups) tmem_ld16(sbuf + 16 * (grp + 1), next);
-          uint32_t pk[8];
+          float2 pw[8];
           if (grp < 2 * warp) {
             const float f = grp < 2 ? to[0] : grp < 4 ? to[1] : to[2];
             const float2 f2 = make_float2(f, f);
@@ -424,12 +425,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float4 o = o4[i];
-              const float2 u = mul2(mul2(make_float2(o.x, o.y), f2),
-                                    make_float2(s[4 * i], s[4 * i + 1]));
-              const float2 v = mul2(mul2(make_float2(o.z, o.w), f2),
-                                    make_float2(s[4 * i + 2], s[4 * i + 3]));
-              pk[2 * i] = pack_bf16(u.x, u.y);
-              pk[2 * i + 1] = pack_bf16(v.x, v.y);
+              pw[2 * i] = mul2(mul2(make_float2(o.x, o.y), f2),
+                               make_float2(s[4 * i], s[4 * i + 1]));
+              pw[2 * i + 1] = mul2(mul2(make_float2(o.z, o.w), f2),
+                                   make_float2(s[4 * i + 2], s[4 * i + 3]));
             }
           } else {
             const float4* in4 = reinterpret_cast<const float4*>(&pr.in[16 * grp]);
@@ -449,16 +448,23 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
               if (4 * i + 1 > own) u.y = 0.0f;
               if (4 * i + 2 > own) v.x = 0.0f;
               if (4 * i + 3 > own) v.y = 0.0f;
-              pk[2 * i] = pack_bf16(u.x, u.y);
-              pk[2 * i + 1] = pack_bf16(v.x, v.y);
+              pw[2 * i] = u;
+              pw[2 * i + 1] = v;
             }
           }
-          // P's columns 8 grp .. lie in columns of S that are already read
-          tmem_st8(sbuf + 8 * grp, pk);
+          // both parts in the place of the columns of S that they come from
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            pk[i] = pack_bf16(pw[i].x, pw[i].y);
+            const float2 rest = sub2(pw[i], unpack_bf16(pk[i]));
+            pk[8 + i] = pack_bf16(rest.x, rest.y);
+          }
+          tmem_st16(sbuf + 16 * grp, pk);
         }
         {
-          const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          for (int grp = groups; grp < 8; ++grp) tmem_st8(sbuf + 8 * grp, none);
+          const uint32_t none[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+          for (int grp = groups; grp < 8; ++grp) tmem_st16(sbuf + 16 * grp, none);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -519,8 +525,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint8_t* vtile = sm + SB_V + (c & 3) * SB_PANEL;
-        const uint32_t ybuf = tm + TM_S + stage * 128 + TM_Y1 + lanes,
-                       y2buf = tm + TM_Y2 + stage * 64 + lanes;
+        const uint32_t ybuf = tm + TM_Y1 + lanes, y2buf = tm + TM_Y2 + stage * 64 + lanes;
 #pragma unroll 1
         for (int part = 0; part < 4; ++part) {
           float y1[16], y2[16];
@@ -622,10 +627,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         const float keep = exp2f((pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
-        ok = wait(BAR_DM + (c & 1), c >> 1);
+        ok = wait(BAR_DM, c);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t dm = tm + TM_DM + (c & 1) * 64 + lanes;
+        const uint32_t dm = tm + TM_DM + lanes;
 #pragma unroll
         for (int part = 0; part < 4; ++part) {
           float r[16];
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_DMFREE + (c & 1)));
+        if (lane == 0) mbar_arrive(bar(BAR_DMFREE));
         if (c + 1 < u0 + w.nb) {
           ok = wait(BAR_HFREE, c);
           if (!ok) break;
@@ -764,8 +769,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     for (; ok && w.get(ba); u0 += w.nb, w.advance(ba))
       for (int c = u0; c < u0 + w.nb && ok; ++c) {
         const uint32_t stage = c & 1, k = k0 + stage * (2 * SB_PANEL >> 4);
-        ok = wait(BAR_KFULL + stage, c >> 1) &&
-             (c < 2 || wait(BAR_DMFREE + stage, (c >> 1) - 1));
+        ok = wait(BAR_KFULL + stage, c >> 1) && (c < 1 || wait(BAR_DMFREE, c - 1));
         for (int qd = 0; qd < 4 && ok; ++qd) {
           const uint32_t use = 4 * c + qd, buf = use & 1;
           ok = wait(BAR_WREADY + buf, use >> 1);
@@ -775,26 +779,27 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             const uint32_t kq = k + qd * (4096 >> 4), wb = w0 + buf * (3 * SB_WPART >> 4);
 #pragma unroll
             for (int i = 0; i < 6; ++i)
-              mma_ss(tm + TM_DM + stage * 64, kq + (i & 1) * (2048 >> 4),
+              mma_ss(tm + TM_DM, kq + (i & 1) * (2048 >> 4),
                      wb + (((i >> 1) * SB_WPART + (i & 1) * 2048) >> 4), dM, qd + i > 0);
             mma_commit(bar(BAR_WFREE + buf));
             if (qd == 3) {
-              mma_commit(bar(BAR_DM + stage));
+              mma_commit(bar(BAR_DM));
               mma_commit(bar(BAR_KFREE + stage));
             }
           }
           __syncwarp();
         }
         // the last quarter is also the sign that v's rows behind the end are zeros
-        ok = ok && wait(BAR_VFULL + (c & 3), c >> 2) && wait(BAR_P + stage, c >> 1);
+        ok = ok && wait(BAR_VFULL + (c & 3), c >> 2) && wait(BAR_P + stage, c >> 1) &&
+             (c < 1 || wait(BAR_YFREE + (stage ^ 1), (c - 1) >> 1));  // Y1 of c - 1 is read
         if (!ok) break;
         tc_fence_after();
         const uint32_t slot = c & 3;
         if (elect_one()) {
           const uint32_t v = v0 + slot * (SB_PANEL >> 4), s = tm + TM_S + stage * 128;
 #pragma unroll
-          for (int i = 0; i < SB_L / 16; ++i)
-            mma_ts(s + TM_Y1, s + 8 * i, v + i * (2048 >> 4), dY1, i > 0);
+          for (int i = 0; i < SB_L / 8; ++i)
+            mma_ts(tm + TM_Y1, s + 8 * i, v + (i >> 1) * (2048 >> 4), dY1, i > 0);
           mma_commit(bar(BAR_Y + stage));
         }
         __syncwarp();

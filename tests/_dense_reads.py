@@ -1,11 +1,10 @@
 """What a read of the dense state adds up, told apart by how a kernel may hold it: the tokens of the
-reader's own block of 128, whose weights the block-wise scan rounds to bf16, and the state
-before that block, which it reads as two bf16 parts.
+reader's own block of 128 and the state before that block.  The block-wise scan holds the weights of
+the first and the values of the second as two bf16 parts.
 
 With |q| |k| |v| d e^{dA} the magnitude of a token's share of a read and |q| |M| that of the state's,
-the first is off by half a step of bf16, 2^-8 of its magnitude, the second by half a step of half
-a step, 2^-16 of it.  Everything else is fp32 and covered by the bound of tests/_dense.py with
-weights = 0."""
+either is off by half a step of half a step of bf16, 2^-16 of its magnitude.  Everything else is
+fp32 and covered by the bound of tests/_dense.py with weights = 0."""
 
 import torch
 
@@ -40,7 +39,7 @@ def magnitudes(k, q, v, dt, A, M, dt_bias, softplus, lens):
 def bound(yb, own, before, gate, act):
     """The bound on a block-wise y before its rounding: yb, from ref.ssm with weights = 0, and the
     roundings of the reads, through the gate."""
-    reads = 2.0 ** -8 * own + 2.0 ** -16 * before
+    reads = 2.0 ** -16 * (own + before)
     return yb + (reads * ref.act64(gate, act).abs() if gate is not None else reads)
 
 

@@ -1,6 +1,6 @@
 """y of the state-space calls on the GPU held to what each kernel may round (_dense_reads.py): the
 step and the token-by-token scan nothing but y itself, the block-wise scan the weights of a
-block's tokens to bf16 and the state before the block to two bf16 parts."""
+block's tokens and the state before the block to two bf16 parts."""
 
 import pytest
 import torch
