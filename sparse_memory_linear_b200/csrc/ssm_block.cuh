@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         }
         tmem_wait_st();
         tc_fence_before();
+        fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(BAR_P + stage));
@@ -498,7 +499,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         if (!ok) break;
         float decay;  // from the block's start up to t
         {
-          const SsmPrep& pr = *prep(c);
+          // used behind the release below: volatile, so that no read is put off or made again
+          const volatile SsmPrep& pr = *prep(c);
           float e = pr.in[t];
 #pragma unroll
           for (int j = 0; j < 3; ++j)
@@ -506,6 +508,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           decay = fast_exp2(e);
         }
         const float2 f2 = make_float2(decay, decay);
+        fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
         uint32_t z[8];
@@ -567,6 +570,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           }
         }
         tc_fence_before();
+        fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(BAR_YFREE + stage));
@@ -623,8 +627,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       for (int c = u0; c < u0 + w.nb; ++c) {
         ok = wait(BAR_PREP + (c & 3), c >> 2);
         if (!ok) break;
-        const SsmPrep& pr = *prep(c);
+        const volatile SsmPrep& pr = *prep(c);  // as in group Y
         const float keep = exp2f((pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]));
+        fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_PREPFREE + (c & 3)));
         ok = wait(BAR_DM, c);
@@ -983,7 +988,8 @@ __global__ void __launch_bounds__(SG_THREADS, 1)
         const uint8_t* vtile = sm + SG_V + stage * SB_PANEL;
         const SsmPrep& pr = *prep(stage);
         const float f = exp2f(carry);
-        carry += (pr.run[0] + pr.run[1]) + (pr.run[2] + pr.run[3]);
+        const volatile float* run = pr.run;  // used behind the stage's release, too
+        carry += (run[0] + run[1]) + (run[2] + run[3]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int qd = 2 * i + grp;  // the group's buffers: qd

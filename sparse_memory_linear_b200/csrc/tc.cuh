@@ -71,7 +71,8 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// This thread's writes to shared memory become visible to the TMA and the matrix unit.
+// This thread's writes to shared memory become visible to the TMA and the matrix unit, and its
+// reads are done before what they overwrite once told.
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

@@ -151,3 +151,22 @@ def test_packed_batches_of_many_sequences(sdm, dt):
     rc, rs, bound = ref.conv(x.double(), w.double(), None, s0, "silu", lens)
     ref.check(yc, rc, bound, "y")
     assert torch.equal(state.double(), rs)
+
+
+@pytest.mark.parametrize("H,G,N,P,lens", [
+    (48, 4, 40, 72, [300, 40, 0, 129, 700, 25, 128, 64, 1, 511]), (37, 1, 128, 64, [2048] * 4),
+    (3, 1, 128, 200, [5000, 100]),
+])
+def test_scans_of_many_pieces_repeat_bit_for_bit(sdm, H, G, N, P, lens):
+    """Tiles are loaded over the ones before as soon as those are released: a read that came too late
+    would give a value of another block now and then."""
+    B, n = len(lens), sum(lens)
+    i, M = ssm_inputs(gen(11), (n,), H, G, N, P, BF, B)
+    cu = torch.tensor([sum(lens[:b]) for b in range(B + 1)], dtype=torch.int32, device=DEV)
+    for gate in (None, randn(gen(12), n, H, P, dtype=BF)):
+        first = None
+        for _ in range(25):
+            Ms = M.clone()
+            y = sdm.sdm_ssm_forward(M=Ms, init="continue", cu=cu, gate=gate, **i)
+            first = first or (y, Ms)
+            assert torch.equal(y, first[0]) and torch.equal(Ms, first[1])
