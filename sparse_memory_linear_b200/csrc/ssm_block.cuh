@@ -25,10 +25,10 @@
 //   sums
 // joined by mbarriers.  A block's work is a chain of short dependent steps; with the steps on
 // warps of their own the chains of successive blocks overlap.  One group for everything took 11
-// us a block, two groups 3.5, these 2.9 (3.8 with a gate; 128 tokens, N = 128, all
-// multiprocessors busy).  No unit is full at that: 46 % of the issue slots are used (9500 warp
-// instructions a block), the matrix unit 39 % of the time, memory less, and a group alone needs
-// 2200 to 2800 of a block's 5500 cycles.  What bounds it is the loop of waits from one group to the
+// us a block, two groups 3.5, these 3.0 (3.8 with a gate; 128 tokens, N = 128, all
+// multiprocessors busy).  No unit is full at that: 46 % of the issue slots are used (10300 warp
+// instructions a block), the matrix unit 42 % of the time, memory less, and a group alone needs
+// about half of a block's 5850 cycles.  What bounds it is the loop of waits from one group to the
 // next; which of them sets the period is not established (q, with its one stage, is one: the
 // load of block c + 1 waits for Y2 of block c, and S of block c + 1 for the load).
 //
