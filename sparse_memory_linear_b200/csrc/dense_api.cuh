@@ -208,9 +208,10 @@ bool tile_map(CUtensorMap* map, const void* p, int width, int heads, long long r
 
 // Which prompts the block-wise scan takes: bf16, at most 128 state rows, and sequences of 24
 // tokens or more (on average, when packed: their own lengths are on the device).  A block costs
-// the same for one token as for 128, the token-by-token scan about 0.27 us a token.  Measured
-// (us, N = 128): 8 heads of 64, 16 tokens 9.7 against 7.2 token by token, 32 tokens 9.5 against
-// 11.7; 8 x 32 heads of 64, 16 tokens 16.2 against 16.3, 32 tokens 16.3 against 27.1.
+// the same for one token as for 128, the token-by-token scan goes by tiles of 16 tokens.  Measured
+// (us, N = 128, calls replayed from a graph): 8 x 32 heads of 64, 16 tokens 14.4 token by token, 23
+// tokens 19.9, 24 to 32 tokens 16.5 in blocks; 8 heads of 64, where neither fills the device, 5.0,
+// 6.6 and 10.2.
 // Its row numbers are 32 bits wide and, in the last block, reach SB_L - 1 rows behind the batch.
 bool ssm_block_fits(const sdm_ssm_shape& s, bool packed) {
   const long long rows = packed ? s.T : (long long)s.B * s.T, length = packed ? s.T / s.B : s.T;
